@@ -18,7 +18,10 @@
  * block with its parallel dense MLP and gamma norms (moe_gemma4_block), the
  * layer with FP8 (e4m3) experts and per-row scales (moe_forward_fp8, with
  * its row quantiser moe_quantize_rows_e4m3), and a permutation that needs
- * no workspace (moe_permute_noalloc).
+ * no workspace (moe_permute_noalloc).  Next to the experts: routing with a
+ * bias for balance (moe_route_balanced), the 8-bit integer product with token
+ * and channel scales (moe_linear_i8, moe_quantize_rows_i8) and the norms
+ * around a block with its gate and residual scale (moe_block_norm).
  *
  * Conventions (every entry point):
  *   - All pointers are DEVICE pointers unless a parameter says otherwise.
@@ -451,6 +454,133 @@ MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const moe_bf16* x,
                                    const float* scale, moe_bf16* out, int32_t* ids_out,
                                    float* w_out, void* ws, size_t ws_bytes,
                                    const moe_forward_opts* opts, cudaStream_t stream);
+
+/*
+ * moe_route_balanced -- routing with a per-expert bias for balance, as routers
+ * trained without an auxiliary loss use it: the bias moves the choice, never
+ * the weight.  Per token, with z its E logits:
+ *   s_e  the score: softmax of z over all E, or sigmoid(z_e)
+ *   c_e  = s_e + bias_e, what the choice compares, as real numbers: ranked in
+ *        64 bits, equal values to the lower id
+ *   n_group > 1: the experts form n_group groups of E / n_group consecutive
+ *        ids; a group's score is the sum of its group_top largest c; the
+ *        topk_group best groups are kept (equal scores to the lower group)
+ *   ids  the k largest c in the kept groups, in descending order
+ *   w_j  = s_id, divided by the sum of the k chosen s when renorm is set
+ *        (0 when that sum is 0), times factor, times scale[id]
+ * Computed in fp64 and rounded once to fp32, but for the softmax's
+ * denominator without renorm, whose terms are fp32 exponentials (relative
+ * error below 1e-6).
+ *   logits [T,E] fp32, bias [E] fp32 or NULL (zeros), scale [E] fp32 or NULL
+ *   opts   NULL is {MOE_SCORE_SOFTMAX, 0, 0, 1, 1, 1.0f}
+ *   ids, w [T,k] out;  load [E] int32 out or NULL: how many of the T*k
+ *          choices fell on each expert (overwritten, also when T == 0)
+ * A logit of -inf or NaN marks an expert that is not available: score 0, c =
+ * -inf, so it comes after every available expert (by id), with weight 0; in a
+ * group's sum it counts as -inf, so a group with fewer than group_top
+ * available experts comes after the others.  +inf counts as the largest
+ * finite value.  A non-finite bias does the same to c (NaN as -inf).  The ids
+ * of a token are always k different valid expert ids, whatever the row holds.
+ * Uses no workspace; shape->H, I, n_shared, act are not read.  Bad options
+ * return MOE_ERR_INVALID_ARG (MOE_ERR_UNSUPPORTED for n_group >
+ * MOE_MAX_GROUPS) before any launch.
+ */
+typedef struct {
+  int32_t scoring;     /* moe_scoring */
+  int32_t n_group;     /* 0 or 1: no groups (topk_group and group_top unused) */
+  int32_t topk_group;  /* 1..n_group, with k <= topk_group * (E / n_group) */
+  int32_t group_top;   /* 1 or 2 largest c summed into a group's score */
+  int32_t renorm;      /* divide the weights by their sum */
+  float factor;        /* finite factor on every weight */
+} moe_balance_opts;
+
+MOE_API moe_status moe_route_balanced(const moe_shape* shape, const float* logits,
+                                      const float* bias, const float* scale,
+                                      const moe_balance_opts* opts, int32_t* ids,
+                                      float* w, int32_t* load, cudaStream_t stream);
+
+/*
+ * moe_quantize_rows_i8 -- per-row dynamic quantisation to 8-bit integers of
+ * bf16 rows src [rows, cols] (cols % 8 == 0, cols <= MOE_MAX_ROW, src 16-byte
+ * aligned) into codes [rows, cols] (8-byte aligned) and scales [rows]:
+ * with amax the row's largest |value|, s = fl32(amax / 127) (1 for an
+ * all-zero row) and code = fl32(v / s) rounded to the nearest integer, ties to
+ * even, within +-127.  Fixed by IEEE fp32 arithmetic, so reproducible bit for
+ * bit.  A row that holds an infinity or a NaN gets codes 0 and a scale that is
+ * not finite (NaN if it holds a NaN), so that products with it are NaN.
+ */
+#define MOE_MAX_ROW 32768
+MOE_API moe_status moe_quantize_rows_i8(const moe_bf16* src, int64_t rows, int cols,
+                                        int8_t* codes, float* scales,
+                                        cudaStream_t stream);
+
+/*
+ * moe_linear_i8 -- the product of 8-bit integer rows with one scale per token
+ * and per channel, as INT8 (W8A8) checkpoints store their dense layers:
+ *   x [T,K] int8 codes, x_scale [T];  w [N,K] int8 codes, w_scale [N]
+ *   v[t,n] = fl(acc) * fl(x_scale[t] * w_scale[n]), acc = sum_k x[t,k] w[n,k]
+ *            exact in 32-bit integers
+ *   gate_act MOE_LINEAR_PLAIN: out [T,N] = v;
+ *            a moe_act: out [T,N/2] = Act(v[t,n]) * v[t, N/2 + n], w holding the
+ *            gate rows first, then the up rows (N even)
+ *   out      bf16 or NULL;  out_f32 fp32 or NULL (the same before its
+ *            rounding); at least one is given
+ *   ws       a workspace of this library or any 256 bytes zeroed once (256-byte
+ *            aligned): only its error word is used (moe_read_error)
+ * Each sum is exact, so the result does not depend on the order it is taken
+ * in: two calls agree bit for bit.  K % 16 == 0 and 16 <= K <= MOE_LINEAR_MAX_K
+ * (the sum of K products of -128 codes stays inside 32 bits), N < 2^22, T < 2^24:
+ * MOE_ERR_UNSUPPORTED otherwise.  x, w, out and out_f32 are 16-byte aligned.
+ */
+#define MOE_LINEAR_PLAIN (-1)
+#define MOE_LINEAR_MAX_K 131056
+MOE_API moe_status moe_linear_i8(int64_t T, int N, int K, const int8_t* x,
+                                 const float* x_scale, const int8_t* w,
+                                 const float* w_scale, int gate_act, moe_bf16* out,
+                                 float* out_f32, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream);
+
+/*
+ * moe_block_norm -- the norms before and after a block, with the block's gate
+ * and the residual scale, in one pass over the rows.  Per token row:
+ *   t  = RMSNorm(y) * post_w                (t = y when post_w is NULL)
+ *   r' = bf16( alpha r + (beta token_gate[t]) * (t * gate) )
+ *   a  = bf16( RMSNorm(r') * pre_w )        the next block's input
+ * and, when codes is given, the int8 codes and scale of the row a as
+ * moe_quantize_rows_i8 makes them.  Without y only the second norm runs, on r
+ * itself; without pre_w only the first half does.  RMSNorm(v) = v *
+ * (1 / sqrt(mean(v^2) + eps)), the mean taken in fp64 and rounded once to fp32;
+ * each product and sum above is one fp32 operation in the order written
+ * (factors that are not given are left out), so a, r' and the codes are
+ * reproducible bit for bit, and equal to the steps taken one by one.
+ *   y, r   [T,H] bf16;  post_w, pre_w, gate [H] bf16;  token_gate [T] fp32
+ *   r_out  [T,H] bf16 out, required with y; may be r itself
+ *   a      [T,H] bf16 out or NULL;  codes [T,H] int8 and scales [T] fp32 out,
+ *          or both NULL; with pre_w at least one of a and codes is given
+ * H % 8 == 0 and H <= MOE_MAX_ROW (MOE_ERR_UNSUPPORTED otherwise), T < 2^24.
+ * Rows and vectors of H are 16-byte aligned (codes 8-byte).  What is not used
+ * must be NULL: without y post_w, gate, token_gate and r_out, without pre_w a,
+ * codes and scales (MOE_ERR_INVALID_ARG otherwise).
+ */
+typedef struct {
+  const moe_bf16* y;
+  const moe_bf16* r;
+  const moe_bf16* post_w;
+  const moe_bf16* gate;
+  const float* token_gate;
+  const moe_bf16* pre_w;
+  float alpha;
+  float beta;
+  float post_eps;
+  float pre_eps;
+  moe_bf16* r_out;
+  moe_bf16* a;
+  int8_t* codes;
+  float* scales;
+} moe_block_norm_params;
+
+MOE_API moe_status moe_block_norm(int64_t T, int H, const moe_block_norm_params* params,
+                                  cudaStream_t stream);
 
 /*
  * moe_read_error -- SYNCHRONISES ``stream``, then returns the status recorded

@@ -30,7 +30,8 @@ EXPORTS = ("moe_layout_capacity", "moe_workspace_size", "moe_router_logits",
            "moe_read_error", "moe_selftest_wait_timeout", "moe_status_string",
            "moe_permute_noalloc", "moe_route_ex", "moe_gemma4_workspace_size",
            "moe_gemma4_block", "moe_quantize_rows_e4m3", "moe_workspace_size_fp8",
-           "moe_forward_fp8")
+           "moe_forward_fp8", "moe_route_balanced", "moe_quantize_rows_i8",
+           "moe_linear_i8", "moe_block_norm")
 
 
 class MoEError(RuntimeError):
@@ -45,11 +46,31 @@ DECODE_MAX_T = 16
 
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 MAX_GROUPS = 32
+ACT_SILU, ACT_GELU_TANH = 0, 1
+LINEAR_PLAIN = -1
+LINEAR_MAX_K = 131056
+MAX_ROW = 32768
 
 
 class moe_route_opts(ctypes.Structure):
     _fields_ = [("scoring", ctypes.c_int32), ("n_group", ctypes.c_int32),
                 ("topk_group", ctypes.c_int32)]
+
+
+class moe_balance_opts(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("factor", ctypes.c_float)]
+
+
+class moe_block_norm_params(ctypes.Structure):
+    _fields_ = [("y", ctypes.c_void_p), ("r", ctypes.c_void_p),
+                ("post_w", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("token_gate", ctypes.c_void_p), ("pre_w", ctypes.c_void_p),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+                ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float),
+                ("r_out", ctypes.c_void_p), ("a", ctypes.c_void_p),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class moe_fp8_experts(ctypes.Structure):
@@ -123,6 +144,13 @@ def _load() -> ctypes.CDLL:
     lib.moe_forward_fp8.argtypes = [S, P, P, ctypes.POINTER(moe_fp8_experts), P, P, P, P,
                                     P, ctypes.c_size_t, ctypes.POINTER(moe_forward_opts), P]
     lib.moe_permute_noalloc.restype = st
+    lib.moe_route_balanced.argtypes = [S, P, P, P, ctypes.POINTER(moe_balance_opts), P, P,
+                                       P, P]
+    lib.moe_quantize_rows_i8.argtypes = [P, ctypes.c_int64, ctypes.c_int, P, P, P]
+    lib.moe_linear_i8.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, P, P, P, P,
+                                  ctypes.c_int, P, P, P, ctypes.c_size_t, P]
+    lib.moe_block_norm.argtypes = [ctypes.c_int64, ctypes.c_int,
+                                   ctypes.POINTER(moe_block_norm_params), P]
     lib.moe_selftest_wait_timeout.argtypes = [P, ctypes.c_size_t,
                                               ctypes.c_uint32, P]
     lib.moe_status_string.argtypes = [st]
@@ -131,7 +159,9 @@ def _load() -> ctypes.CDLL:
                  "moe_expert_ffn",
                  "moe_combine",
                  "moe_forward", "moe_forward_ex", "moe_read_error", "moe_gemma4_block",
-                 "moe_selftest_wait_timeout", "moe_quantize_rows_e4m3", "moe_forward_fp8"):
+                 "moe_selftest_wait_timeout", "moe_quantize_rows_e4m3", "moe_forward_fp8",
+                 "moe_route_balanced", "moe_quantize_rows_i8", "moe_linear_i8",
+                 "moe_block_norm"):
         getattr(lib, name).restype = st
     return lib
 
@@ -392,3 +422,91 @@ def moe_forward_fp8(shape, x, logits, weights: moe_fp8_experts, scale, out, ws,
                                _p(scale), _p(out), _p(ids_out), _p(w_out), _p(ws),
                                ws.numel(), ctypes.byref(opts), _stream(stream)),
            "moe_forward_fp8")
+
+
+# ------------------------------------------------ next to the expert products
+#
+# These calls are made once or twice per block and token step, so their own
+# cost counts at small T: the checks read tensor attributes only.  Unlike a raw
+# pointer, a tensor of the wrong type, size or device is refused here.
+
+def _q(t, dtype, numel, what):
+    """The address of a contiguous CUDA tensor of ``numel`` ``dtype`` values on
+    the current device, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of {numel} values, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device")
+    return t.data_ptr()
+
+
+def _s(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+def balance_opts(scoring=SCORE_SOFTMAX, n_group=1, topk_group=1, group_top=1, renorm=True,
+                 factor=1.0) -> moe_balance_opts:
+    """The options of moe_route_balanced; make them once and pass them on."""
+    return moe_balance_opts(scoring, n_group, topk_group, group_top, int(bool(renorm)), factor)
+
+
+def moe_route_balanced(shape, logits, bias, scale, ids, w, load=None, opts=None, stream=None):
+    """Routing with a balance bias: logits [T,E] fp32, ``bias`` [E] fp32 or None
+    (moves the choice, not the weight), ``scale`` [E] fp32 or None; ids [T,k]
+    int32 and w [T,k] fp32 out, ``load`` [E] int32 out or None (choices per
+    expert, overwritten); ``opts`` from balance_opts()."""
+    T, E, k = shape.T, shape.E, shape.k
+    f32, i32 = torch.float32, torch.int32
+    _check(lib.moe_route_balanced(
+        shape, _q(logits, f32, T * E, "logits"), _q(bias, f32, E, "bias"),
+        _q(scale, f32, E, "scale"), opts, _q(ids, i32, T * k, "ids"), _q(w, f32, T * k, "w"),
+        _q(load, i32, E, "load"), _s(stream)), "moe_route_balanced")
+
+
+def moe_quantize_rows_i8(src, codes, scales, stream=None):
+    """Per-row dynamic int8 quantisation of bf16 rows src [R, C] into codes
+    (int8 [R, C]) and scales (fp32 [R])."""
+    R, C = src.shape
+    _check(lib.moe_quantize_rows_i8(
+        _q(src, torch.bfloat16, R * C, "src"), R, C, _q(codes, torch.int8, R * C, "codes"),
+        _q(scales, torch.float32, R, "scales"), _s(stream)), "moe_quantize_rows_i8")
+
+
+def moe_linear_i8(x, x_scale, w, w_scale, out, ws, gate_act=None, out_f32=None, stream=None):
+    """The int8 product x [T,K] @ w [N,K]^T with scales per token and per channel
+    into ``out`` [T,N] bf16 (or None) and ``out_f32`` [T,N] fp32 (or None).
+    ``gate_act`` None, or ACT_SILU / ACT_GELU_TANH: w holds gate rows, then up
+    rows, and out is [T,N/2] = Act(gate) * up.  ``ws``: at least 256 bytes
+    (uint8), zeroed once; its error word is read by moe_read_error."""
+    T, K = x.shape
+    N = w.shape[0]
+    n_out = T * (N if gate_act is None else N // 2)
+    i8, f32 = torch.int8, torch.float32
+    _check(lib.moe_linear_i8(
+        T, N, K, _q(x, i8, T * K, "x"), _q(x_scale, f32, T, "x_scale"), _q(w, i8, N * K, "w"),
+        _q(w_scale, f32, N, "w_scale"), LINEAR_PLAIN if gate_act is None else gate_act,
+        _q(out, torch.bfloat16, n_out, "out"), _q(out_f32, f32, n_out, "out_f32"),
+        _q(ws, torch.uint8, ws.numel(), "ws"), ws.numel(), _s(stream)), "moe_linear_i8")
+
+
+def moe_block_norm(r, y=None, post_w=None, gate=None, token_gate=None, alpha=1.0, beta=1.0,
+                   post_eps=1e-6, pre_w=None, pre_eps=1e-6, r_out=None, a=None, codes=None,
+                   scales=None, stream=None):
+    """The norms around a block, on the residual rows r [T,H] bf16: with the
+    block's output y [T,H], r_out = alpha r + (beta token_gate) (RMSNorm(y)
+    post_w gate); with pre_w, a = RMSNorm(r_out) pre_w and / or its int8 codes
+    [T,H] and scales [T].  post_w, pre_w and gate [H] bf16, token_gate [T]
+    fp32.  r_out may be r."""
+    T, H = r.shape
+    n, bf, f32 = T * H, torch.bfloat16, torch.float32
+    prm = moe_block_norm_params(
+        _q(y, bf, n, "y"), _q(r, bf, n, "r"), _q(post_w, bf, H, "post_w"),
+        _q(gate, bf, H, "gate"), _q(token_gate, f32, T, "token_gate"),
+        _q(pre_w, bf, H, "pre_w"), alpha, beta, post_eps, pre_eps, _q(r_out, bf, n, "r_out"),
+        _q(a, bf, n, "a"), _q(codes, torch.int8, n, "codes"), _q(scales, f32, T, "scales"))
+    _check(lib.moe_block_norm(T, H, prm, _s(stream)), "moe_block_norm")

@@ -1,0 +1,283 @@
+// norm.cu -- the norms around a block (moe_block_norm) and the int8 row
+// quantiser (moe_quantize_rows_i8).  Per token row, each step one fp32
+// operation:
+//   t  = y (1 / sqrt(mean(y^2) + eps)) post_w        (t = y without post_w)
+//   r' = bf16(alpha r + (beta token_gate) (t gate))
+//   a  = bf16(r' (1 / sqrt(mean(r'^2) + eps)) pre_w)
+//   codes: s = amax(a) / 127, rint(a / s)
+// The quantiser is the last step alone, on the rows it is given.
+//
+// Bound: HBM.  A row is read once and kept in registers (8 bf16 values per
+// 16-byte vector, VPT vectors per thread) through its up to three reductions,
+// so every input byte is read once and every output byte written once.  One
+// block per row.
+//
+// The means are taken in double (a square of a bf16 value is exact in fp32),
+// so that they round to the same fp32 value whatever the order of the sum, and
+// with IEEE divisions and square roots the rows and their codes come out the
+// same bits as the steps taken one by one.
+#include <cmath>
+
+#include "internal.cuh"
+
+namespace moe {
+namespace {
+
+struct RowParams {
+  const uint4 *y, *r, *post_w, *gate, *pre_w;
+  const float* token_gate;
+  float alpha, beta, post_eps, pre_eps;
+  uint4 *r_out, *a;
+  uint2* codes;
+  float* scales;
+  int vec;  // 16-byte vectors per row
+  int H;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+__device__ __forceinline__ double squares(const float (&f)[8]) {
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += (double)f[i] * (double)f[i];
+  return s;
+}
+
+// Sum over the block; red holds one value per warp.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
+  __syncthreads();  // red may still be read by the previous call
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  double s = 0.0;
+  for (int i = 0; i < n; ++i) s += red[i];
+  return s;
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
+  __syncthreads();
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  uint32_t m = 0;
+  for (int i = 0; i < n; ++i) m = max(m, red[i]);
+  return m;
+}
+
+// 1 / sqrt(mean + eps), IEEE fp32, of the mean of squares rounded to fp32
+__device__ __forceinline__ float rms_inverse(double ss, int H, float eps) {
+  return 1.0f / sqrtf((float)(ss / (double)H) + eps);
+}
+
+// Largest |value| of eight bf16 values as their 15-bit patterns, which order
+// like the values, with infinity and then NaN above them.
+__device__ __forceinline__ uint32_t abs_bits(const uint4& v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+
+__device__ __forceinline__ uint32_t code(float v, float s) {
+  // an infinite or NaN row (s not finite) gives v / s = 0 or NaN: code 0
+  const int c = __float2int_rn(__fdiv_rn(v, s));
+  return (uint32_t)max(-127, min(127, c)) & 0xffu;
+}
+
+template <int VPT>
+__global__ void __launch_bounds__(1024)
+rows_kernel(const RowParams p) {
+  __shared__ double red[32];
+  __shared__ uint32_t redm[32];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t = blockIdx.x, base = t * p.vec;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  uint4 r[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = tid + j * nt;
+    r[j] = c < p.vec ? p.r[base + c] : make_uint4(0, 0, 0, 0);
+  }
+  if (p.y) {
+    uint4 y[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * nt;
+      y[j] = c < p.vec ? p.y[base + c] : make_uint4(0, 0, 0, 0);
+    }
+    float inv = 1.0f;
+    if (p.post_w) {
+      double ss = 0.0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        float f[8];
+        unpack8(y[j], f);
+        ss += squares(f);
+      }
+      inv = rms_inverse(block_sum(ss, red), p.H, p.post_eps);
+    }
+    const float m = p.token_gate ? __fmul_rn(p.beta, p.token_gate[t]) : p.beta;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * nt;
+      if (c < p.vec) {
+        float f[8], g[8], o[8];
+        unpack8(y[j], f);
+        if (p.post_w) {
+          unpack8(__ldg(p.post_w + c), g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(f[i], inv), g[i]);
+        }
+        if (p.gate) {
+          unpack8(__ldg(p.gate + c), g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], g[i]);
+        }
+        unpack8(r[j], o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          o[i] = __fadd_rn(__fmul_rn(p.alpha, o[i]), __fmul_rn(m, f[i]));
+        r[j] = pack8(o);
+        p.r_out[base + c] = r[j];
+      }
+    }
+  }
+  if (p.pre_w) {
+    double ss = 0.0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float f[8];
+      unpack8(r[j], f);
+      ss += squares(f);
+    }
+    const float inv = rms_inverse(block_sum(ss, red), p.H, p.pre_eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * nt;
+      if (c < p.vec) {
+        float f[8], g[8];
+        unpack8(r[j], f);
+        unpack8(__ldg(p.pre_w + c), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(f[i], inv), g[i]);
+        r[j] = pack8(f);
+        if (p.a) p.a[base + c] = r[j];
+      }
+    }
+  }
+  if (p.codes) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) m = max(m, abs_bits(r[j]));
+    const float amax = __uint_as_float(block_max(m, redm) << 16);
+    const float s = amax == 0.0f ? 1.0f : __fdiv_rn(amax, 127.0f);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * nt;
+      if (c < p.vec) {
+        float f[8];
+        unpack8(r[j], f);
+        uint2 o;
+        o.x = code(f[0], s) | code(f[1], s) << 8 | code(f[2], s) << 16 | code(f[3], s) << 24;
+        o.y = code(f[4], s) | code(f[5], s) << 8 | code(f[6], s) << 16 | code(f[7], s) << 24;
+        p.codes[base + c] = o;
+      }
+    }
+    if (tid == 0) p.scales[t] = s;
+  }
+}
+
+cudaError_t launch_rows(int64_t rows, const RowParams& p, cudaStream_t st) {
+  const int vpt = p.vec <= 128 ? 1 : p.vec <= 256 ? 2 : 4;
+  int nt = (p.vec + vpt - 1) / vpt;
+  nt = (nt + 31) / 32 * 32;
+  auto kern = vpt == 1 ? rows_kernel<1> : vpt == 2 ? rows_kernel<2> : rows_kernel<4>;
+  return launch_ex(kern, dim3((unsigned)rows), dim3(nt), 0, st, false, p);
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_quantize_rows_i8(const moe_bf16* src, int64_t rows, int cols, int8_t* codes,
+                                float* scales, cudaStream_t stream) {
+  if (rows < 0 || cols <= 0 || cols % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if (cols > MOE_MAX_ROW || rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!src || !codes || !scales || !aligned(src, 16) || !aligned(codes, 8))
+    return MOE_ERR_INVALID_ARG;
+  RowParams p{};
+  p.r = reinterpret_cast<const uint4*>(src);
+  p.codes = reinterpret_cast<uint2*>(codes);
+  p.scales = scales;
+  p.vec = cols / 8;
+  p.H = cols;
+  return launch_rows(rows, p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_block_norm(int64_t T, int H, const moe_block_norm_params* q,
+                          cudaStream_t stream) {
+  if (T < 0 || H <= 0 || !q) return MOE_ERR_INVALID_ARG;
+  if (H % 8 != 0 || H > MOE_MAX_ROW || T >= (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;
+  if (!std::isfinite(q->alpha) || !std::isfinite(q->beta)) return MOE_ERR_INVALID_ARG;
+  for (const float eps : {q->post_eps, q->pre_eps})
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  // what a half that does not run would use, and a half without an output
+  if (!q->y && (q->post_w || q->gate || q->token_gate || q->r_out)) return MOE_ERR_INVALID_ARG;
+  if (!q->pre_w && (q->a || q->codes || q->scales)) return MOE_ERR_INVALID_ARG;
+  if (!q->y && !q->pre_w) return MOE_ERR_INVALID_ARG;
+  if ((q->codes == nullptr) != (q->scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!q->r || (q->y && !q->r_out) || (q->pre_w && !q->a && !q->codes))
+    return MOE_ERR_INVALID_ARG;
+  for (const void* v : {(const void*)q->y, (const void*)q->r, (const void*)q->post_w,
+                        (const void*)q->gate, (const void*)q->pre_w, (const void*)q->r_out,
+                        (const void*)q->a})
+    if (!aligned(v, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(q->codes, 8)) return MOE_ERR_INVALID_ARG;
+  auto vec = [](const moe_bf16* v) { return reinterpret_cast<const uint4*>(v); };
+  RowParams p{};
+  p.y = vec(q->y);
+  p.r = vec(q->r);
+  p.post_w = vec(q->post_w);
+  p.gate = vec(q->gate);
+  p.pre_w = vec(q->pre_w);
+  p.token_gate = q->token_gate;
+  p.alpha = q->alpha;
+  p.beta = q->beta;
+  p.post_eps = q->post_eps;
+  p.pre_eps = q->pre_eps;
+  p.r_out = reinterpret_cast<uint4*>(q->r_out);
+  p.a = reinterpret_cast<uint4*>(q->a);
+  p.codes = reinterpret_cast<uint2*>(q->codes);
+  p.scales = q->scales;
+  p.vec = H / 8;
+  p.H = H;
+  return launch_rows(T, p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"
