@@ -29,7 +29,6 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 192;
 constexpr int kABytes = 128 * 128;   // 128 weight rows x 128 bytes of K
 constexpr int kMaxStages = 12;
 constexpr uint64_t kTimeoutNs = 1000000000ull;  // 1 s per wait
@@ -49,7 +48,6 @@ struct LinParams {
   int stages;
   int MT, TT;   // weight tiles (of CG x 128 rows) and token tiles (nsub x tn)
   int panel;    // token tiles per panel of the tile order
-  int split;    // CTAs that share K
   uint32_t cols;  // TMEM columns
   __nv_bfloat16* out;
   float* out_f32;
@@ -75,6 +73,12 @@ __device__ __forceinline__ float lin_act(int act, float g) {
   return __fdividef(g, 1.0f + __expf(e));
 }
 
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
 struct LinTile {
   int mt;
   int64_t t0;  // first token
@@ -92,74 +96,105 @@ __device__ __forceinline__ LinTile lin_tile(int64_t u, const LinParams& p) {
   return LinTile{(int)mt, (pn * p.panel + in - mt * pw) * p.nsub * p.tn};
 }
 
-// What the epilogue needs of a lane: its channel and scales.
+// A lane of the epilogue: its channel and scales.  The lanes of a pair (plain:
+// lanes 2i and 2i + 1, neighbouring channels; gated: l and l + 16, gate and up
+// row of a channel) each finish one of two token columns for both their rows.
 template <bool GATED>
 struct LaneOut {
-  int n;        // output channel
-  bool ok;
-  float s0, s1;  // plain: scales of channels n, n + 1 of the even lane; gated: gate, up
-  int lane;
+  int n;         // first output channel
+  bool ok;       // it exists (plain: n; n + 1 is checked where it is stored)
+  bool hi;       // second lane of the pair: takes the second column
+  float s0, s1;  // scales of the pair's two rows
 
-  __device__ __forceinline__ void init(const LinParams& p, int row, int ln) {
-    lane = ln;
+  __device__ __forceinline__ void init(const LinParams& p, int row, int lane) {
     if (GATED) {
-      n = (row >> 5) * 16 + (ln & 15);
+      hi = lane >= 16;
+      n = (row >> 5) * 16 + (lane & 15);
       ok = n < p.NO;
       s0 = ok ? __ldg(p.ws + n) : 0.f;
       s1 = ok ? __ldg(p.ws + p.NO + n) : 0.f;
     } else {
-      n = row;
-      ok = n < p.N;
-      const float own = ok ? __ldg(p.ws + n) : 0.f;
-      const float other = __shfl_xor_sync(0xffffffffu, own, 1);
-      s0 = (ln & 1) ? other : own;
-      s1 = (ln & 1) ? own : other;
+      hi = (lane & 1) != 0;
+      n = row & ~1;
+      ok = n < p.NO;
+      s0 = ok ? __ldg(p.ws + n) : 0.f;
+      s1 = n + 1 < p.NO ? __ldg(p.ws + n + 1) : 0.f;
     }
   }
 
-  // Two token columns c and c + 1 of this lane's row; t: token of column c; the
-  // token scales sx (of c) and sy (of c + 1).
-  __device__ __forceinline__ void store2(const LinParams& p, int64_t t, int32_t a, int32_t b,
-                                         float sx, float sy) const {
-    // partners swap one value, so that each lane holds both rows of one token
-    const bool up = GATED ? lane >= 16 : (lane & 1) != 0;
-    const int32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, GATED ? 16 : 1);
-    const int64_t tok = t + (up ? 1 : 0);
-    const float s = up ? sy : sx;
-    const float v0 = __fmul_rn((float)(up ? got : a), __fmul_rn(s, s0));
-    const float v1 = __fmul_rn((float)(up ? b : got), __fmul_rn(s, s1));
-    if (tok >= p.T) return;
+  // NP pairs of columns of this lane's row: a[j], b[j] are columns of tokens
+  // t + stride j and t + stride j + 1 (tokens from t_end on are not stored),
+  // sx[j] the scale of the one this lane finishes.  No branch between the pairs, so that their chains overlap.
+  template <int NP>
+  __device__ __forceinline__ void store(const LinParams& p, int64_t t, int64_t t_end, int stride,
+                                        const int32_t (&a)[NP], const int32_t (&b)[NP],
+                                        const float (&sx)[NP]) const {
+    float v0[NP], v1[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int32_t got = __shfl_xor_sync(0xffffffffu, hi ? a[j] : b[j], GATED ? 16 : 1);
+      v0[j] = __fmul_rn((float)(hi ? got : a[j]), __fmul_rn(sx[j], s0));
+      v1[j] = __fmul_rn((float)(hi ? b[j] : got), __fmul_rn(sx[j], s1));
+    }
+    const int64_t tok = t + (hi ? 1 : 0);
+    int64_t left = t_end - tok;  // pairs j < left / stride are real
+    left = left > 0 ? (left + stride - 1) / stride : 0;
+    const int nv = ok ? (int)(left < NP ? left : NP) : 0;
+    const int64_t at = tok * p.NO + n, step = (int64_t)stride * p.NO;
     if (GATED) {
-      if (!ok) return;
-      const float v = lin_act(p.act, v0) * v1;
-      const int64_t at = tok * p.NO + n;
-      if (p.out) p.out[at] = __float2bfloat16_rn(v);
-      if (p.out_f32) p.out_f32[at] = v;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) v0[j] = lin_act(p.act, v0[j]) * v1[j];
+      if (p.out) {
+        __nv_bfloat16* o = p.out + at;
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+          if (j < nv) o[j * step] = __float2bfloat16_rn(v0[j]);
+      }
+      if (p.out_f32) {
+        float* o = p.out_f32 + at;
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+          if (j < nv) o[j * step] = v0[j];
+      }
+    } else if ((p.NO & 1) == 0) {
+      if (p.out) {
+        __nv_bfloat16* o = p.out + at;
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+          if (j < nv)
+            *reinterpret_cast<__nv_bfloat162*>(o + j * step) = __floats2bfloat162_rn(v0[j], v1[j]);
+      }
+      if (p.out_f32) {
+        float* o = p.out_f32 + at;
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+          if (j < nv) *reinterpret_cast<float2*>(o + j * step) = make_float2(v0[j], v1[j]);
+      }
     } else {
-      const int m = n & ~1;  // channels m, m + 1
-      const int64_t at = tok * p.NO + m;
-      if (m + 1 < p.N && (p.NO & 1) == 0) {
-        if (p.out) *reinterpret_cast<__nv_bfloat162*>(p.out + at) = __floats2bfloat162_rn(v0, v1);
-        if (p.out_f32) *reinterpret_cast<float2*>(p.out_f32 + at) = make_float2(v0, v1);
-      } else {
-        if (m < p.N) {
-          if (p.out) p.out[at] = __float2bfloat16_rn(v0);
-          if (p.out_f32) p.out_f32[at] = v0;
+      const bool two = n + 1 < p.NO;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        if (j < nv) {
+          if (p.out) p.out[at + j * step] = __float2bfloat16_rn(v0[j]);
+          if (p.out_f32) p.out_f32[at + j * step] = v0[j];
         }
-        if (m + 1 < p.N) {
-          if (p.out) p.out[at + 1] = __float2bfloat16_rn(v1);
-          if (p.out_f32) p.out_f32[at + 1] = v1;
+        if (j < nv && two) {
+          if (p.out) p.out[at + j * step + 1] = __float2bfloat16_rn(v1[j]);
+          if (p.out_f32) p.out_f32[at + j * step + 1] = v1[j];
         }
       }
     }
   }
 };
 
-template <int CG, bool GATED, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+// CG = 2: CTA pairs walk the tiles.  CG = 1: one tile per cluster of SPLIT CTAs
+// that share K.  EW epilogue warps.
+template <int CG, bool GATED, int SPLIT, int EW>
+__global__ void __launch_bounds__(64 + 32 * EW, 1)
 linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmX, const LinParams p) {
-  static_assert(!(SPLIT && CG == 2), "K is split over single CTAs");
+  static_assert(CG == 1 || SPLIT == 1, "K is split over single CTAs");
+  static_assert(EW == 4 || EW == 8, "one or two warps for each 32 accumulator lanes");
   extern __shared__ uint8_t smem_raw[];
   __shared__ LinCtl ctl_s;
   LinCtl* ctl = &ctl_s;
@@ -172,7 +207,7 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
   const uint32_t sB = base + p.stages * kABytes;
   volatile int32_t* abort_flag = &ctl->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = (CG == 2 || SPLIT) ? cluster_ctarank() : 0u;
+  const uint32_t rank = (CG == 2 || SPLIT > 1) ? cluster_ctarank() : 0u;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -181,7 +216,7 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&ctl->tmem_full[a]), 1);
-      mbar_init(smem_u32(&ctl->tmem_empty[a]), 4 * CG);  // one per epilogue warp
+      mbar_init(smem_u32(&ctl->tmem_empty[a]), EW * CG);  // one per epilogue warp
     }
     mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort_flag = 0;
@@ -203,14 +238,11 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
 
-  // tiles: one per cluster with SPLIT (grid = tiles x split), else a walk
-  const int64_t unit0 = SPLIT ? (int64_t)(blockIdx.x / p.split)
-                        : CG == 2 ? (int64_t)cluster_id_x() : (int64_t)blockIdx.x;
   const int64_t total = (int64_t)p.MT * p.TT;
-  const int64_t step = SPLIT ? total
-                       : CG == 2 ? (int64_t)nclusters_x() : (int64_t)gridDim.x;
-  const int kb0 = SPLIT ? (int)(rank * p.KB / p.split) : 0;
-  const int kb1 = SPLIT ? (int)((rank + 1) * p.KB / p.split) : p.KB;
+  const int64_t unit0 = CG == 2 ? (int64_t)cluster_id_x() : (int64_t)(blockIdx.x / SPLIT);
+  const int64_t step = CG == 2 ? (int64_t)nclusters_x() : total;
+  const int kb0 = (int)(rank * p.KB / SPLIT) * (CG == 1);
+  const int kb1 = CG == 1 ? (int)((rank + 1) * p.KB / SPLIT) : p.KB;
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
@@ -323,8 +355,11 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
     }
   } else {
     // ----------------------------------------------------------- epilogue
-    // Warp w reads TMEM lanes [32 (w % 4), 32 (w % 4) + 32).
+    // Warp w reads TMEM lanes [32 (w % 4), 32 (w % 4) + 32); with eight warps,
+    // two take the 32-column chunks of the same lanes in turn.
     const int q = warp & 3;
+    constexpr int HALVES = EW / 4;
+    const int c_first = 32 * ((warp - 2) >> 2);
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t empty0 = CG == 2 ? mapa_shared(smem_u32(&ctl->tmem_empty[0]), 0) : 0u;
     const uint32_t empty1 = CG == 2 ? mapa_shared(smem_u32(&ctl->tmem_empty[1]), 0) : 0u;
@@ -340,30 +375,34 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + lanes + buf * 256;
-      if constexpr (SPLIT) {
-        // partial sums [column][128 rows] over the ring, which is idle now
-        int32_t* part = reinterpret_cast<int32_t*>(gbase);
-        for (int c = 0; c < p.tn; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(tb + c, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < p.tn) part[(c + j) * 128 + q * 32 + lane] = (int32_t)v[j];
-        }
-        break;  // one tile per cluster; finished below
-      } else {
       for (int s = 0; s < p.nsub; ++s) {
         const int64_t ts = tl.t0 + (int64_t)s * p.tn;
-        for (int c = 0; c < p.tn; c += 32) {
-          if (ts + c >= p.T) break;
+        for (int c = c_first; c < p.tn && ts + c < p.T; c += 32 * HALVES) {
           uint32_t v[32];
           tmem_ld32(tb + s * 256 + c, v);
-          const float sx = ts + c + lane < p.T ? __ldg(p.xs + ts + c + lane) : 0.f;
+          if constexpr (SPLIT > 1) {
+            // partial sums [column][128 rows] over the ring, which is idle now
+            int32_t* part = reinterpret_cast<int32_t*>(gbase) + q * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            if (c + j < p.tn)
-              lo.store2(p, ts + c + j, (int32_t)v[j], (int32_t)v[j + 1],
-                        __shfl_sync(0xffffffffu, sx, j), __shfl_sync(0xffffffffu, sx, j + 1));
+            for (int j = 0; j < 32; ++j)
+              if (c + j < p.tn) part[(c + j) * 128] = (int32_t)v[j];
+          } else {
+            const float sl = ts + c + lane < p.T ? __ldg(p.xs + ts + c + lane) : 0.f;
+            // columns past tn belong to the next sub-tile or to nobody
+            const int64_t t_end = ts + p.tn < p.T ? ts + p.tn : p.T;
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              int32_t a[8], b[8];
+              float sx[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                a[j] = (int32_t)v[h + 2 * j];
+                b[j] = (int32_t)v[h + 2 * j + 1];
+                sx[j] = __shfl_sync(0xffffffffu, sl, h + 2 * j + (lo.hi ? 1 : 0));
+              }
+              lo.template store<8>(p, ts + c + h, t_end, 2, a, b, sx);
+            }
+          }
         }
       }
       // this warp is done with the accumulator: one arrival per warp (on CTA
@@ -377,39 +416,56 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
           mbar_arrive(smem_u32(&ctl->tmem_empty[buf]));
       }
       if (++buf == p.nbuf) { buf = 0; buf_phase ^= 1u; }
-      }
     }
   }
 
-  if (SPLIT) {
+  if constexpr (SPLIT > 1) {
     __syncwarp();
     cluster_sync();  // every CTA's partial sums are in its shared memory
     if (warp >= 2 && !*abort_flag) {
-      // columns c = 2 rank, 2 rank + 1, then 2 split further on
-      const int q = warp & 3, row = q * 32 + lane;
+      // CTA r finishes the column pairs r, r + SPLIT, ..., NP at a time; the
+      // EW / 4 warps of a row quarter take turns
+      constexpr int NP = 16 / SPLIT < 4 ? 16 / SPLIT : 4;
+      const int q = warp & 3, row = q * 32 + lane, half = (warp - 2) >> 2;
       const LinTile tl = lin_tile(unit0, p);
       LaneOut<GATED> lo;
       lo.init(p, tl.mt * 128 + row, lane);
-      const uint32_t mine = smem_u32(gbase) + row * 4;
-      for (int c = 2 * (int)rank; c < p.tn && tl.t0 + c < p.T; c += 2 * p.split) {
-        int32_t a = 0, b = 0;
-        for (int r = 0; r < p.split; ++r) {
-          const uint32_t src = mapa_shared(mine + c * 512, r);
-          int32_t u, v;
-          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(u) : "r"(src));
-          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(src + 512));
-          a += u;
-          b += v;
+      uint32_t src[SPLIT];
+#pragma unroll
+      for (int r = 0; r < SPLIT; ++r) src[r] = mapa_shared(smem_u32(gbase) + row * 4, r);
+      constexpr int GROUP = 2 * SPLIT * NP;  // columns of one turn, at most 32
+      for (int c0 = GROUP * half; c0 < p.tn && tl.t0 + c0 < p.T; c0 += GROUP * (EW / 4)) {
+        const int c = c0 + 2 * (int)rank;
+        int32_t a[NP], b[NP];
+        float sx[NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const int64_t tok = tl.t0 + c + 2 * SPLIT * j + (lo.hi ? 1 : 0);
+          sx[j] = tok < p.T ? __ldg(p.xs + tok) : 0.f;
+          a[j] = b[j] = 0;
         }
-        const float sx = __ldg(p.xs + tl.t0 + c);
-        const float sy = tl.t0 + c + 1 < p.T ? __ldg(p.xs + tl.t0 + c + 1) : 0.f;
-        lo.store2(p, tl.t0 + c, a, b, sx, sy);
+#pragma unroll
+        for (int r = 0; r < SPLIT; ++r) {
+          int32_t ua[NP], ub[NP];
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const uint32_t at = src[r] + (uint32_t)(c + 2 * SPLIT * j) * 512u;
+            ua[j] = ld_cluster_s32(at);
+            ub[j] = ld_cluster_s32(at + 512u);
+          }
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            a[j] += ua[j];
+            b[j] += ub[j];
+          }
+        }
+        lo.template store<NP>(p, tl.t0 + c, p.T, 2 * SPLIT, a, b, sx);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (CG == 2 || SPLIT) cluster_sync();  // no peer still uses this CTA's memory or TMEM
+  if (CG == 2 || SPLIT > 1) cluster_sync();  // no peer still uses this CTA's memory or TMEM
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
@@ -458,10 +514,12 @@ cudaError_t make_gated_map(CUtensorMap* m, const void* ptr, uint64_t K, uint64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int CG, bool GATED, bool SPLIT>
-cudaError_t launch_linear(LinParams& p, const int8_t* x, const int8_t* w, int K, int clusters,
-                          cudaStream_t st) {
-  auto kern = linear_i8_kernel<CG, GATED, SPLIT>;
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <int CG, bool GATED, int SPLIT, int EW>
+cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, int K,
+                          int clusters, cudaStream_t st) {
+  auto kern = linear_i8_kernel<CG, GATED, SPLIT, EW>;
   CUtensorMap mw, mx;
   cudaError_t e = GATED ? make_gated_map(&mw, w, K, p.NO) : make_tma_map_e4m3(&mw, w, K, p.N, 128);
   if (e == cudaSuccess) e = make_tma_map_e4m3(&mx, x, K, p.T, p.tn / CG);
@@ -476,26 +534,26 @@ cudaError_t launch_linear(LinParams& p, const int8_t* x, const int8_t* w, int K,
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDev) ready[dev].store(true);
   }
-  const int per = SPLIT ? p.split : CG;
+  constexpr int per = CG * SPLIT;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * per));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(64 + 32 * EW);
   const size_t ring = (size_t)p.stages * (kABytes + (size_t)p.tn / CG * 128 * p.nsub);
-  cfg.dynamicSmemBytes = 1024 + std::max(ring, SPLIT ? (size_t)p.tn * 512 : (size_t)0);
+  // one 512-byte row of partial sums per column, read in groups of up to 32
+  const size_t part = SPLIT > 1 ? (size_t)ceil_div(p.tn, 32) * 32 * 512 : 0;
+  cfg.dynamicSmemBytes = 1024 + std::max(ring, part);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)per;
+  attr[1].val.clusterDim.x = per;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = per > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, mw, mx, (const LinParams)p);
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
 }
-
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <bool GATED>
 cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cudaStream_t st) {
@@ -512,12 +570,15 @@ cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cud
     p.cols = p.tn <= 32 ? 32 : p.tn <= 64 ? 64 : 128;
     int split = 1;
     while (split < 8 && p.MT * split < sms && 2 * split <= p.KB) split *= 2;
-    p.split = split;
+    // all CTAs resident at once where two or three fit an SM
+    const int res = std::min(3, ceil_div((int64_t)p.MT * split, sms));
     const int stage = kABytes + p.tn * 128;
-    p.stages = std::min({kMaxStages, (kSmemMax - 2048) / stage, ceil_div(p.KB, split)});
-    return launch_linear<1, GATED, true>(p, x, w, K, p.MT, st);
+    p.stages = std::min({kMaxStages, (kSmemMax / res - 3 * 1024) / stage, ceil_div(p.KB, split)});
+    if (split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, p.MT, st);
+    if (split == 2) return launch_linear<1, GATED, 2, 4>(p, x, w, K, p.MT, st);
+    if (split == 4) return launch_linear<1, GATED, 4, 4>(p, x, w, K, p.MT, st);
+    return launch_linear<1, GATED, 8, 4>(p, x, w, K, p.MT, st);
   }
-  p.split = 1;
   p.TT = ceil_div(p.T, 256);
   p.tn = 32 * ceil_div(ceil_div(p.T, p.TT), 32);
   p.nbuf = 2;
@@ -527,7 +588,7 @@ cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cud
   const int stage = kABytes + p.tn / 2 * 128;
   p.stages = std::min(kMaxStages, (kSmemMax - 2048) / stage);
   const int64_t tiles = (int64_t)p.MT * p.TT;
-  return launch_linear<2, GATED, false>(p, x, w, K, (int)std::min<int64_t>(sms / 2, tiles), st);
+  return launch_linear<2, GATED, 1, 8>(p, x, w, K, (int)std::min<int64_t>(sms / 2, tiles), st);
 }
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
