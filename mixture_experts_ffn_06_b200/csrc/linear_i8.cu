@@ -10,14 +10,16 @@
 // each epilogue warp, 16 gate rows and then the matching 16 up rows (one 3D
 // TMA box over w [2, I, K]), so lane l's partner is lane l + 16.
 //
-// Two forms, both with one TMA warp, one MMA warp and four epilogue warps:
-//   few tokens  (bound by streaming w): a tile per cluster of up to 8 CTAs that
+// Up to 8 tokens take a form without the tensor cores (linear_i8_few_kernel
+// below).  The others, both with one TMA warp, one MMA warp and four epilogue warps:
+//   9 to 128 tokens (bound by streaming w): a tile per cluster of up to 8 CTAs that
 //               split K; each parks its partial sums in shared memory and adds
 //               up a slice of the columns over all CTAs' (integers: the order
 //               of the sum does not matter);
-//   many tokens (bound by the tensor cores and by L2 -> shared memory): CTA
-//               pairs (M = 256) walk the tiles, two accumulators in TMEM so that
-//               a tile's epilogue runs beside the next one's MMAs.
+//   more (bound by the tensor cores, under the power limit): persistent CTAs or
+//               CTA pairs (M = 256) walk the tiles, two accumulators in TMEM so
+//               that a tile's epilogue runs beside the next one's MMAs, or one of
+//               twice the columns, which reads each weight tile half as often.
 // Every mbarrier wait is bounded (tc_ptx.cuh); after a timeout the block
 // records MOE_ERR_TIMEOUT, waits for its own copies and MMAs and frees TMEM.
 #include <algorithm>
@@ -46,7 +48,7 @@ struct LinParams {
   int nsub;     // MMAs (token sub-tiles) that share a weight tile
   int nbuf;     // accumulators in TMEM
   int stages;
-  int MT, TT;   // weight tiles (of CG x 128 rows) and token tiles (nsub x tn)
+  uint32_t MT, TT;  // weight tiles (of CG x 128 rows) and token tiles (nsub x tn)
   int panel;    // token tiles per panel of the tile order
   uint32_t cols;  // TMEM columns
   __nv_bfloat16* out;
@@ -64,10 +66,37 @@ struct LinCtl {
   int32_t abort_flag;
 };
 
+// mbar_wait, with the first tries made here: the timed wait reads the global
+// timer, which costs as much as several k-blocks.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity,
+                                         volatile int32_t* abort_flag, uint32_t* err) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_test(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, kTimeoutNs, err);
+}
+__device__ __forceinline__ bool wait_for_cluster(uint32_t bar, uint32_t parity,
+                                                 volatile int32_t* abort_flag, uint32_t* err) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_test_cluster(bar, parity)) return true;
+  return mbar_wait_cluster(bar, parity, abort_flag, kTimeoutNs, err);
+}
+
+// Two fp32 products at once, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+
 // Both activations as g sigma(.): 0.5 (1 + tanh v) = sigma(2v) does not cancel
 // where v is large and negative.
-__device__ __forceinline__ float lin_act(int act, float g) {
-  const float e = act == MOE_ACT_SILU
+template <int ACT>
+__device__ __forceinline__ float lin_act(float g) {
+  const float e = ACT == MOE_ACT_SILU
                       ? -g
                       : -1.5957691216057308f * fmaf(0.044715f * g, g * g, g);  // -2 v
   return __fdividef(g, 1.0f + __expf(e));
@@ -79,6 +108,15 @@ __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
   return v;
 }
 
+// 16 bytes of a weight row, which pass through once
+__device__ __forceinline__ int4 ld_stream(const int4* p) {
+  int4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 struct LinTile {
   int mt;
   int64_t t0;  // first token
@@ -87,13 +125,12 @@ struct LinTile {
 // Tile u: panels of ``panel`` token tiles, then the weight tile, then the token
 // tile inside the panel, so that the tiles running at once share weight tiles
 // and the panel's tokens stay in L2 while the weights pass by once per panel.
-__device__ __forceinline__ LinTile lin_tile(int64_t u, const LinParams& p) {
-  const int64_t per = (int64_t)p.panel * p.MT;
-  const int64_t pn = u / per, in = u - pn * per;
-  const int64_t left = p.TT - pn * p.panel;
-  const int64_t pw = left < p.panel ? left : p.panel;
-  const int64_t mt = in / pw;
-  return LinTile{(int)mt, (pn * p.panel + in - mt * pw) * p.nsub * p.tn};
+__device__ __forceinline__ LinTile lin_tile(uint32_t u, const LinParams& p) {
+  const uint32_t per = (uint32_t)p.panel * p.MT;
+  const uint32_t pn = u / per, in = u - pn * per;
+  const uint32_t pw = min((uint32_t)p.panel, p.TT - pn * p.panel);
+  const uint32_t mt = in / pw;
+  return LinTile{(int)mt, (int64_t)(pn * p.panel + in - mt * pw) * p.nsub * p.tn};
 }
 
 // A lane of the epilogue: its channel and scales.  The lanes of a pair (plain:
@@ -133,54 +170,79 @@ struct LaneOut {
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int32_t got = __shfl_xor_sync(0xffffffffu, hi ? a[j] : b[j], GATED ? 16 : 1);
-      v0[j] = __fmul_rn((float)(hi ? got : a[j]), __fmul_rn(sx[j], s0));
-      v1[j] = __fmul_rn((float)(hi ? b[j] : got), __fmul_rn(sx[j], s1));
+      const float2 s = mul2(make_float2(sx[j], sx[j]), make_float2(s0, s1));
+      const float2 v = mul2(make_float2((float)(hi ? got : a[j]), (float)(hi ? b[j] : got)), s);
+      v0[j] = v.x;
+      v1[j] = v.y;
+    }
+    if (GATED) {
+      if (p.act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) v0[j] = lin_act<MOE_ACT_SILU>(v0[j]) * v1[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) v0[j] = lin_act<MOE_ACT_GELU_TANH>(v0[j]) * v1[j];
+      }
     }
     const int64_t tok = t + (hi ? 1 : 0);
-    int64_t left = t_end - tok;  // pairs j < left / stride are real
-    left = left > 0 ? (left + stride - 1) / stride : 0;
-    const int nv = ok ? (int)(left < NP ? left : NP) : 0;
-    const int64_t at = tok * p.NO + n, step = (int64_t)stride * p.NO;
-    if (GATED) {
+    const int64_t step = (int64_t)stride * p.NO;
+    const bool full = t + (NP - 1) * stride + 1 < t_end;
+    if (GATED && NP % 2 == 0 && full && !p.out_f32 && (p.NO & 1) == 0) {
+      // neighbouring channels swap one of two tokens, for 4-byte stores
+      const bool odd = (n & 1) != 0;
+      __nv_bfloat16* o = p.out + (tok + (odd ? stride : 0)) * p.NO + (n & ~1);
 #pragma unroll
-      for (int j = 0; j < NP; ++j) v0[j] = lin_act(p.act, v0[j]) * v1[j];
-      if (p.out) {
-        __nv_bfloat16* o = p.out + at;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-          if (j < nv) o[j * step] = __float2bfloat16_rn(v0[j]);
+      for (int j = 0; j + 1 < NP; j += 2, o += 2 * step) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v0[j], v0[j + 1]);
+        const uint32_t mine = *reinterpret_cast<const uint32_t*>(&h);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+        // even: (mine.lo, other.lo) of token j; odd: (other.hi, mine.hi) of j + 1
+        const uint32_t w = __byte_perm(mine, other, odd ? 0x3276 : 0x5410);
+        if (ok) *reinterpret_cast<uint32_t*>(o) = w;
       }
-      if (p.out_f32) {
-        float* o = p.out_f32 + at;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-          if (j < nv) o[j * step] = v0[j];
-      }
-    } else if ((p.NO & 1) == 0) {
-      if (p.out) {
-        __nv_bfloat16* o = p.out + at;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-          if (j < nv)
-            *reinterpret_cast<__nv_bfloat162*>(o + j * step) = __floats2bfloat162_rn(v0[j], v1[j]);
-      }
-      if (p.out_f32) {
-        float* o = p.out_f32 + at;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-          if (j < nv) *reinterpret_cast<float2*>(o + j * step) = make_float2(v0[j], v1[j]);
-      }
+      return;
+    }
+    if (!ok) return;
+    const int64_t at = tok * p.NO + n;
+    if (full) {
+      write<NP>(p, at, step, NP, v0, v1);
     } else {
-      const bool two = n + 1 < p.NO;
+      int64_t left = t_end - tok;  // pairs j < left / stride are real
+      left = left > 0 ? (left + stride - 1) / stride : 0;
+      write<NP>(p, at, step, (int)(left < NP ? left : NP), v0, v1);
+    }
+  }
+
+  template <int NP>
+  __device__ __forceinline__ void write(const LinParams& p, int64_t at, int64_t step, int nv,
+                                        const float (&v0)[NP], const float (&v1)[NP]) const {
+    if (p.out) {
+      __nv_bfloat16* o = p.out + at;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        if (j < nv) {
-          if (p.out) p.out[at + j * step] = __float2bfloat16_rn(v0[j]);
-          if (p.out_f32) p.out_f32[at + j * step] = v0[j];
+      for (int j = 0; j < NP; ++j, o += step) {
+        if (j >= nv) continue;
+        if (GATED) {
+          *o = __float2bfloat16_rn(v0[j]);
+        } else if ((p.NO & 1) == 0) {
+          *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(v0[j], v1[j]);
+        } else {
+          o[0] = __float2bfloat16_rn(v0[j]);
+          if (n + 1 < p.NO) o[1] = __float2bfloat16_rn(v1[j]);
         }
-        if (j < nv && two) {
-          if (p.out) p.out[at + j * step + 1] = __float2bfloat16_rn(v1[j]);
-          if (p.out_f32) p.out_f32[at + j * step + 1] = v1[j];
+      }
+    }
+    if (p.out_f32) {
+      float* o = p.out_f32 + at;
+#pragma unroll
+      for (int j = 0; j < NP; ++j, o += step) {
+        if (j >= nv) continue;
+        if (GATED) {
+          *o = v0[j];
+        } else if ((p.NO & 1) == 0) {
+          *reinterpret_cast<float2*>(o) = make_float2(v0[j], v1[j]);
+        } else {
+          o[0] = v0[j];
+          if (n + 1 < p.NO) o[1] = v1[j];
         }
       }
     }
@@ -197,6 +259,7 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
   static_assert(EW == 4 || EW == 8, "one or two warps for each 32 accumulator lanes");
   extern __shared__ uint8_t smem_raw[];
   __shared__ LinCtl ctl_s;
+  __shared__ __align__(16) float sx_s[EW][32];
   LinCtl* ctl = &ctl_s;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -238,9 +301,10 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
 
-  const int64_t total = (int64_t)p.MT * p.TT;
-  const int64_t unit0 = CG == 2 ? (int64_t)cluster_id_x() : (int64_t)(blockIdx.x / SPLIT);
-  const int64_t step = CG == 2 ? (int64_t)nclusters_x() : total;
+  // (fewer than 2^31 tiles: the host checks)
+  const uint32_t total = (uint32_t)p.MT * p.TT;
+  const uint32_t unit0 = CG == 2 ? cluster_id_x() : blockIdx.x / SPLIT;
+  const uint32_t step = CG == 2 ? nclusters_x() : SPLIT == 1 ? gridDim.x : total;
   const int kb0 = (int)(rank * p.KB / SPLIT) * (CG == 1);
   const int kb1 = CG == 1 ? (int)((rank + 1) * p.KB / SPLIT) : p.KB;
 
@@ -250,13 +314,16 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
       int stage = 0;
       uint32_t phase = 0, filled = 0, last = 0;  // bit s: stage s filled, its parity
       bool ok = true;
-      for (int64_t u = unit0; ok && u < total; u += step) {
+      for (uint32_t u = unit0; ok && u < total; u += step) {
         const LinTile tl = lin_tile(u, p);
         const int mrow = (tl.mt * CG + (int)(CG == 2 ? rank : 0)) * (GATED ? 64 : 128);
         const int64_t tr = tl.t0 + (CG == 2 ? (int64_t)rank * (p.tn / 2) : 0);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, kTimeoutNs,
-                         p.err)) {
+        // each weight tile starts elsewhere in K and wraps round (integer sums
+        // do not mind), so that the CTAs do not all read the same lines of x
+        // at the same time
+        int kb = kb0 + (int)(tl.mt * 5u % (uint32_t)(kb1 - kb0));
+        for (int i = kb0; i < kb1; ++i, kb = kb + 1 < kb1 ? kb + 1 : kb0) {
+          if (!wait_for(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
@@ -307,15 +374,15 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
-      for (int64_t u = unit0; ok && u < total; u += step) {
+      for (uint32_t u = unit0; ok && u < total; u += step) {
         const uint32_t eb = smem_u32(&ctl->tmem_empty[buf]);
-        ok = CG == 2 ? mbar_wait_cluster(eb, buf_phase ^ 1u, abort_flag, kTimeoutNs, p.err)
-                     : mbar_wait(eb, buf_phase ^ 1u, abort_flag, kTimeoutNs, p.err);
+        ok = CG == 2 ? wait_for_cluster(eb, buf_phase ^ 1u, abort_flag, p.err)
+                     : wait_for(eb, buf_phase ^ 1u, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * 256;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(smem_u32(&ctl->full[stage]), phase, abort_flag, kTimeoutNs, p.err)) {
+          if (!wait_for(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err)) {
             ok = false;
             break;
           }
@@ -365,40 +432,66 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
     const uint32_t empty1 = CG == 2 ? mapa_shared(smem_u32(&ctl->tmem_empty[1]), 0) : 0u;
     int buf = 0;
     uint32_t buf_phase = 0;
-    for (int64_t u = unit0; u < total; u += step) {
+    for (uint32_t u = unit0; u < total; u += step) {
       const LinTile tl = lin_tile(u, p);
       LaneOut<GATED> lo;
       lo.init(p, (tl.mt * CG + (int)(CG == 2 ? rank : 0)) * 128 + q * 32 + lane, lane);
-      const bool got = mbar_wait(smem_u32(&ctl->tmem_full[buf]), buf_phase, abort_flag,
-                                 kTimeoutNs, p.err);
+      // token scales of this warp's chunks, requested before the wait
+      float sl[4];
+      auto token_scales = [&](int64_t ts) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t tok = ts + c_first + 32 * HALVES * i + lane;
+          sl[i] = tok < p.T ? __ldg(p.xs + tok) : 0.f;
+        }
+      };
+      if (SPLIT == 1) token_scales(tl.t0);
+      const bool got = wait_for(smem_u32(&ctl->tmem_full[buf]), buf_phase, abort_flag, p.err);
       // warp-uniform decision; also reconverges the warp for tcgen05.ld
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + lanes + buf * 256;
-      for (int s = 0; s < p.nsub; ++s) {
-        const int64_t ts = tl.t0 + (int64_t)s * p.tn;
-        for (int c = c_first; c < p.tn && ts + c < p.T; c += 32 * HALVES) {
+      if constexpr (SPLIT > 1) {
+        // partial sums [column][128 rows] over the ring, which is idle now
+        int32_t* part = reinterpret_cast<int32_t*>(gbase) + q * 32 + lane;
+#pragma unroll 1
+        for (int c = c_first; c < p.tn; c += 32 * HALVES) {
           uint32_t v[32];
-          tmem_ld32(tb + s * 256 + c, v);
-          if constexpr (SPLIT > 1) {
-            // partial sums [column][128 rows] over the ring, which is idle now
-            int32_t* part = reinterpret_cast<int32_t*>(gbase) + q * 32 + lane;
+          tmem_ld32(tb + c, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < p.tn) part[(c + j) * 128] = (int32_t)v[j];
-          } else {
-            const float sl = ts + c + lane < p.T ? __ldg(p.xs + ts + c + lane) : 0.f;
-            // columns past tn belong to the next sub-tile or to nobody
-            const int64_t t_end = ts + p.tn < p.T ? ts + p.tn : p.T;
+          for (int j = 0; j < 32; ++j)
+            if (c + j < p.tn) part[(c + j) * 128] = (int32_t)v[j];
+        }
+      } else {
+        float* sx_w = sx_s[warp - 2];
+        for (int s = 0; s < p.nsub; ++s) {
+          const int64_t ts = tl.t0 + (int64_t)s * p.tn;
+          // columns past tn belong to the next sub-tile or to nobody
+          const int64_t t_end = ts + p.tn < p.T ? ts + p.tn : p.T;
+          if (s > 0) token_scales(ts);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c_first + 32 * HALVES * i;
+            if (c >= p.tn || ts + c >= p.T) break;
+            uint32_t v[32];
+            tmem_ld32(tb + s * 256 + c, v);
+            // the scales by the parity of their token: a lane reads the 16 of its
+            // own columns as four vectors
+            __syncwarp();
+            sx_w[(lane & 1) * 16 + (lane >> 1)] = sl[i];
+            __syncwarp();
 #pragma unroll
             for (int h = 0; h < 32; h += 16) {
               int32_t a[8], b[8];
               float sx[8];
 #pragma unroll
+              for (int j = 0; j < 8; j += 4)
+                *reinterpret_cast<float4*>(sx + j) = *reinterpret_cast<const float4*>(
+                    sx_w + (lo.hi ? 16 : 0) + h / 2 + j);
+#pragma unroll
               for (int j = 0; j < 8; ++j) {
                 a[j] = (int32_t)v[h + 2 * j];
                 b[j] = (int32_t)v[h + 2 * j + 1];
-                sx[j] = __shfl_sync(0xffffffffu, sl, h + 2 * j + (lo.hi ? 1 : 0));
               }
               lo.template store<8>(p, ts + c + h, t_end, 2, a, b, sx);
             }
@@ -450,8 +543,11 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
             const uint32_t at = src[r] + (uint32_t)(c + 2 * SPLIT * j) * 512u;
-            ua[j] = ld_cluster_s32(at);
-            ub[j] = ld_cluster_s32(at + 512u);
+            ua[j] = ub[j] = 0;
+            if (tl.t0 + c + 2 * SPLIT * j < p.T) {
+              ua[j] = ld_cluster_s32(at);
+              ub[j] = ld_cluster_s32(at + 512u);
+            }
           }
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
@@ -474,6 +570,86 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
     else
       tmem_dealloc(tmem_base, p.cols);
   }
+}
+
+// ---------------------------------------------------------- at most 8 tokens
+// A warp takes R weight rows (gated: R / 2 channels, the gate rows then their up
+// rows) and NT tokens, each lane every 32nd 16-byte vector of K, with four-way
+// integer dot products and one warp reduction per (row, token) at the end.  No
+// barrier, no shared memory and no tensor map: all of a warp's weight loads of a
+// step are in flight before the first is used, and the x rows come from L1.
+template <int NT, int R, bool GATED>
+__global__ void __launch_bounds__(128)
+linear_i8_few_kernel(const int4* __restrict__ x, const int4* __restrict__ w, int vec,
+                     const LinParams p) {
+  constexpr int U = 8 / R < 2 ? 2 : 8 / R;  // vectors of each row in flight per lane
+  constexpr int CH = GATED ? R / 2 : R;     // channels of a warp
+  const int lane = threadIdx.x & 31;
+  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * CH;
+  pdl_wait();
+  pdl_trigger();
+  if (n0 >= p.NO) return;
+  const int T = (int)p.T;
+  const int4* row[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int ch = min(n0 + r % CH, p.NO - 1);  // past the end: read, not stored
+    row[r] = w + (int64_t)(GATED && r >= CH ? p.NO + ch : ch) * vec;
+  }
+  int acc[R][NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[r][t] = 0;
+  for (int v0 = lane; v0 < vec; v0 += 32 * U) {
+    int4 a[R][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        a[r][u] = make_int4(0, 0, 0, 0);
+        if (v0 + 32 * u < vec) a[r][u] = ld_stream(row[r] + v0 + 32 * u);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (v0 + 32 * u >= vec) break;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (t >= T) break;
+        const int4 b = __ldg(x + (int64_t)t * vec + v0 + 32 * u);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          acc[r][t] = __dp4a(a[r][u].x, b.x, acc[r][t]);
+          acc[r][t] = __dp4a(a[r][u].y, b.y, acc[r][t]);
+          acc[r][t] = __dp4a(a[r][u].z, b.z, acc[r][t]);
+          acc[r][t] = __dp4a(a[r][u].w, b.w, acc[r][t]);
+        }
+      }
+    }
+  }
+  // lane ch * NT + t finishes channel n0 + ch of token t
+  int mine = 0, up = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
+      if (lane == (r % CH) * NT + t) {
+        if (r < CH) mine = sum;
+        else up = sum;
+      }
+    }
+  const int t = lane % NT, n = n0 + lane / NT;
+  if (lane >= CH * NT || t >= T || n >= p.NO) return;
+  const float sx = __ldg(p.xs + t);
+  float v = __fmul_rn((float)mine, __fmul_rn(sx, __ldg(p.ws + n)));
+  if (GATED) {
+    const float u = __fmul_rn((float)up, __fmul_rn(sx, __ldg(p.ws + p.NO + n)));
+    v = (p.act == MOE_ACT_SILU ? lin_act<MOE_ACT_SILU>(v) : lin_act<MOE_ACT_GELU_TANH>(v)) * u;
+  }
+  const int64_t at = (int64_t)t * p.NO + n;
+  if (p.out) p.out[at] = __float2bfloat16_rn(v);
+  if (p.out_f32) p.out_f32[at] = v;
 }
 
 // ------------------------------------------------------------------- host
@@ -530,7 +706,7 @@ cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, 
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev || !ready[dev].load()) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemMax - (int)sizeof(LinCtl));
+                             kSmemMax - (int)(sizeof(LinCtl) + sizeof(float) * 32 * EW));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDev) ready[dev].store(true);
   }
@@ -555,39 +731,102 @@ cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, 
   return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
 }
 
+template <int NT, bool GATED>
+cudaError_t launch_few(const LinParams& p, const int8_t* x, const int8_t* w, int K,
+                       cudaStream_t st) {
+  // two rows per warp spread a small weight over every SM; four share each
+  // x vector between more rows once there are enough
+  const bool four = p.N >= 4 * 16 * device_sm_count();
+  const int rows = four ? 4 : 2;
+  const int blocks = ceil_div(p.NO, 4 * (GATED ? rows / 2 : rows));
+  auto kern = four ? linear_i8_few_kernel<NT, 4, GATED> : linear_i8_few_kernel<NT, 2, GATED>;
+  return launch_ex(kern, dim3(blocks), dim3(128), 0, st, true,
+                   reinterpret_cast<const int4*>(x), reinterpret_cast<const int4*>(w), K / 16, p);
+}
+
+// The tile of the many-token form: the one with the least estimated time.  Per
+// k-block an SM (or each SM of a pair) takes about max(360, 180 + 1.1 c) ns for c
+// token columns (measured on B200, c = 64 to 512: 365 ns up to 128, 390 at 192, 430
+// at 256, 515 at 320, 740 at 512); a tile's epilogue about 1000 + 14 c ns, which
+// runs beside the next tile's MMAs while two accumulators fit (c <= 256).
+struct LinPlan {
+  int cg, tn, nsub, TT;
+  double ns;
+};
+
+LinPlan plan_tiles(int64_t T, int mt128, int KB, int sms) {
+  LinPlan best{1, 0, 0, 0, 0.0};
+  for (int nsub = 1; nsub <= 2; ++nsub) {
+    const int tt0 = ceil_div(T, 256 * nsub);
+    for (int tt = tt0; tt <= tt0 + 4; ++tt) {
+      const int per = ceil_div(T, (int64_t)tt * nsub);
+      // CTA pairs halve what each SM loads of the tokens: worth it for long sums
+      // over several rounds (K = 4096, T = 4096: 355 against 368 us; K = 2816,
+      // T = 8192: 91 against 86 us) and for 512 columns (T = 512: 31 against 36 us)
+      int cg = 1;
+      int64_t rounds = 0;
+      int tn = 0, TT = 0;
+      for (;;) {
+        tn = 16 * cg * ceil_div(per, 16 * cg);
+        TT = ceil_div(T, (int64_t)tn * nsub);
+        rounds = (ceil_div(mt128, cg) * (int64_t)TT + sms / cg - 1) / (sms / cg);
+        if (cg == 1 && ((KB >= 32 && rounds >= 4) || nsub * tn > 384)) cg = 2;
+        else break;
+      }
+      if (tn > 256) continue;
+      const double c = (double)tn * nsub;
+      const double body = KB * std::max(360.0, 180.0 + 1.1 * c), epi = 1000.0 + 14.0 * c;
+      const double ns = nsub == 1 ? (rounds - 1) * std::max(body, epi) + body + epi
+                                  : rounds * (body + epi);
+      if (best.tn == 0 || ns < best.ns) best = LinPlan{cg, tn, nsub, TT, ns};
+    }
+  }
+  return best;
+}
+
 template <bool GATED>
 cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cudaStream_t st) {
   const int sms = device_sm_count();
   const int rows = GATED ? 64 : 128;  // output channels of 128 weight rows
+  if (p.T <= 1) return launch_few<1, GATED>(p, x, w, K, st);
+  if (p.T <= 2) return launch_few<2, GATED>(p, x, w, K, st);
+  if (p.T <= 4) return launch_few<4, GATED>(p, x, w, K, st);
+  if (p.T <= 8) return launch_few<8, GATED>(p, x, w, K, st);
   p.KB = ceil_div(K, 128);
-  p.nsub = 1;
+  const int mt128 = ceil_div(p.NO, rows);
   if (p.T <= 128) {
+    p.nsub = 1;
     p.tn = 16 * ceil_div(p.T, 16);
     p.nbuf = 1;
     p.TT = 1;
     p.panel = 1;
-    p.MT = ceil_div(p.NO, rows);
+    p.MT = mt128;
     p.cols = p.tn <= 32 ? 32 : p.tn <= 64 ? 64 : 128;
     int split = 1;
-    while (split < 8 && p.MT * split < sms && 2 * split <= p.KB) split *= 2;
+    while (split < 8 && mt128 * split < sms && 2 * split <= p.KB) split *= 2;
     // all CTAs resident at once where two or three fit an SM
-    const int res = std::min(3, ceil_div((int64_t)p.MT * split, sms));
+    const int res = std::min(3, ceil_div((int64_t)mt128 * split, sms));
     const int stage = kABytes + p.tn * 128;
     p.stages = std::min({kMaxStages, (kSmemMax / res - 3 * 1024) / stage, ceil_div(p.KB, split)});
-    if (split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, p.MT, st);
-    if (split == 2) return launch_linear<1, GATED, 2, 4>(p, x, w, K, p.MT, st);
-    if (split == 4) return launch_linear<1, GATED, 4, 4>(p, x, w, K, p.MT, st);
-    return launch_linear<1, GATED, 8, 4>(p, x, w, K, p.MT, st);
+    if (split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, mt128, st);
+    if (split == 2) return launch_linear<1, GATED, 2, 4>(p, x, w, K, mt128, st);
+    if (split == 4) return launch_linear<1, GATED, 4, 4>(p, x, w, K, mt128, st);
+    return launch_linear<1, GATED, 8, 4>(p, x, w, K, mt128, st);
   }
-  p.TT = ceil_div(p.T, 256);
-  p.tn = 32 * ceil_div(ceil_div(p.T, p.TT), 32);
-  p.nbuf = 2;
+  const LinPlan pl = plan_tiles(p.T, mt128, p.KB, sms);
+  p.tn = pl.tn;
+  p.nsub = pl.nsub;
+  p.nbuf = pl.nsub == 1 ? 2 : 1;
+  p.TT = pl.TT;
   p.panel = 16;
-  p.MT = ceil_div(p.NO, 2 * rows);
+  p.MT = ceil_div(mt128, pl.cg);
   p.cols = 512;
-  const int stage = kABytes + p.tn / 2 * 128;
-  p.stages = std::min(kMaxStages, (kSmemMax - 2048) / stage);
+  const int stage = kABytes + p.tn / pl.cg * 128 * p.nsub;
+  p.stages = std::min(kMaxStages, (kSmemMax - 3 * 1024) / stage);
   const int64_t tiles = (int64_t)p.MT * p.TT;
+  if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  if (pl.cg == 1)
+    return launch_linear<1, GATED, 1, 8>(p, x, w, K, (int)std::min<int64_t>(sms, tiles), st);
   return launch_linear<2, GATED, 1, 8>(p, x, w, K, (int)std::min<int64_t>(sms / 2, tiles), st);
 }
 
