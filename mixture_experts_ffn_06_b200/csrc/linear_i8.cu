@@ -10,9 +10,9 @@
 // each epilogue warp, 16 gate rows and then the matching 16 up rows (one 3D
 // TMA box over w [2, I, K]), so lane l's partner is lane l + 16.
 //
-// Up to 8 tokens take a form without the tensor cores (linear_i8_few_kernel
-// below).  The others, both with one TMA warp, one MMA warp and four epilogue warps:
-//   9 to 128 tokens (bound by streaming w): a tile per cluster of up to 8 CTAs that
+// The fewest tokens take a form of small independent blocks
+// (linear_i8_few_kernel below).  The others, both with one TMA warp, one MMA warp and four epilogue warps:
+//   up to 128 tokens (bound by streaming w): a tile per cluster of up to 8 CTAs that
 //               split K; each parks its partial sums in shared memory and adds
 //               up a slice of the columns over all CTAs' (integers: the order
 //               of the sum does not matter);
@@ -572,82 +572,99 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
   }
 }
 
-// ---------------------------------------------------------- at most 8 tokens
-// A warp takes R weight rows (gated: R / 2 channels, the gate rows then their up
-// rows) and NT tokens, each lane every 32nd 16-byte vector of K, with four-way
-// integer dot products and one warp reduction per (row, token) at the end.  No
-// barrier, no shared memory and no tensor map: all of a warp's weight loads of a
-// step are in flight before the first is used, and the x rows come from L1.
-template <int NT, int R, bool GATED>
-__global__ void __launch_bounds__(128)
+// --------------------------------------------------------- at most 16 tokens
+// A block of W warps takes 16 weight rows (gated: 8 gate rows and the
+// matching 8 up rows) and all tokens; the warps take 64-byte steps of K in turn.
+// mma.sync m16n8k32 with the weights as A and the tokens as B, both read
+// straight into fragments: lane (g, q) loads 16 bytes at 16 q of a step, of the
+// rows g and g + 8 and of token g, and uses the four words as the K slots of two
+// MMAs.  That permutes K the same way on both sides.  U steps are requested
+// before the first is used; nothing but the final sum over the warps meets at a
+// barrier.
+
+__device__ __forceinline__ void mma_i8(int (&d)[4], int a0, int a1, int a2, int a3, int b0,
+                                       int b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int NB, bool GATED, int W>  // NB tiles of 8 tokens
+__global__ void __launch_bounds__(32 * W)
 linear_i8_few_kernel(const int4* __restrict__ x, const int4* __restrict__ w, int vec,
                      const LinParams p) {
-  constexpr int U = 8 / R < 2 ? 2 : 8 / R;  // vectors of each row in flight per lane
-  constexpr int CH = GATED ? R / 2 : R;     // channels of a warp
-  const int lane = threadIdx.x & 31;
-  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * CH;
+  constexpr int U = W == 16 ? 3 : 4;
+  __shared__ int part[W][NB * 4][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int n0 = blockIdx.x * (GATED ? 8 : 16);
+  const int T = (int)p.T;
+  // rows past the end: read the last one, store nothing
+  const int ra = min(n0 + g, p.NO - 1);
+  const int rb = GATED ? p.NO + ra : min(n0 + g + 8, p.NO - 1);
+  const int4* wa = w + (int64_t)ra * vec;
+  const int4* wb = w + (int64_t)rb * vec;
   pdl_wait();
   pdl_trigger();
-  if (n0 >= p.NO) return;
-  const int T = (int)p.T;
-  const int4* row[R];
+  int acc[NB][4];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int ch = min(n0 + r % CH, p.NO - 1);  // past the end: read, not stored
-    row[r] = w + (int64_t)(GATED && r >= CH ? p.NO + ch : ch) * vec;
-  }
-  int acc[R][NT];
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int i = 0; i < 4; ++i) acc[b][i] = 0;
+  const int4 zero = make_int4(0, 0, 0, 0);
+  for (int v0 = 4 * warp + q; v0 - q < vec; v0 += 4 * W * U) {
+    int4 a[U], c[U], t[U][NB];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[r][t] = 0;
-  for (int v0 = lane; v0 < vec; v0 += 32 * U) {
-    int4 a[R][U];
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + 4 * W * u;
+      a[u] = v < vec ? ld_stream(wa + v) : zero;
+      c[u] = v < vec ? ld_stream(wb + v) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + 4 * W * u;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int tok = 8 * b + g;
+        t[u][b] = v < vec && tok < T ? __ldg(x + (int64_t)tok * vec + v) : zero;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        a[r][u] = make_int4(0, 0, 0, 0);
-        if (v0 + 32 * u < vec) a[r][u] = ld_stream(row[r] + v0 + 32 * u);
+      for (int b = 0; b < NB; ++b) {
+        mma_i8(acc[b], a[u].x, c[u].x, a[u].y, c[u].y, t[u][b].x, t[u][b].y);
+        mma_i8(acc[b], a[u].z, c[u].z, a[u].w, c[u].w, t[u][b].z, t[u][b].w);
       }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (v0 + 32 * u >= vec) break;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (t >= T) break;
-        const int4 b = __ldg(x + (int64_t)t * vec + v0 + 32 * u);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          acc[r][t] = __dp4a(a[r][u].x, b.x, acc[r][t]);
-          acc[r][t] = __dp4a(a[r][u].y, b.y, acc[r][t]);
-          acc[r][t] = __dp4a(a[r][u].z, b.z, acc[r][t]);
-          acc[r][t] = __dp4a(a[r][u].w, b.w, acc[r][t]);
-        }
-      }
-    }
   }
-  // lane ch * NT + t finishes channel n0 + ch of token t
-  int mine = 0, up = 0;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
-      if (lane == (r % CH) * NT + t) {
-        if (r < CH) mine = sum;
-        else up = sum;
-      }
-    }
-  const int t = lane % NT, n = n0 + lane / NT;
-  if (lane >= CH * NT || t >= T || n >= p.NO) return;
-  const float sx = __ldg(p.xs + t);
-  float v = __fmul_rn((float)mine, __fmul_rn(sx, __ldg(p.ws + n)));
+    for (int i = 0; i < 4; ++i) part[warp][b * 4 + i][lane] = acc[b][i];
+  __syncthreads();
+  // a thread finishes one token of rows g and g + 8: entries i and i + 2
+  if (threadIdx.x >= NB * 64) return;
+  const int b = threadIdx.x >> 6, i = (threadIdx.x >> 5) & 1;
+  int s0 = 0, s1 = 0;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    s0 += part[k][b * 4 + i][lane];
+    s1 += part[k][b * 4 + i + 2][lane];
+  }
+  const int tok = 8 * b + 2 * q + i, n = n0 + g;
+  if (tok >= T || n >= p.NO) return;
+  const float sx = __ldg(p.xs + tok);
+  const int64_t at = (int64_t)tok * p.NO + n;
+  float v = __fmul_rn((float)s0, __fmul_rn(sx, __ldg(p.ws + n)));
   if (GATED) {
-    const float u = __fmul_rn((float)up, __fmul_rn(sx, __ldg(p.ws + p.NO + n)));
+    const float u = __fmul_rn((float)s1, __fmul_rn(sx, __ldg(p.ws + p.NO + n)));
     v = (p.act == MOE_ACT_SILU ? lin_act<MOE_ACT_SILU>(v) : lin_act<MOE_ACT_GELU_TANH>(v)) * u;
+  } else if (n + 8 < p.NO) {
+    const float u = __fmul_rn((float)s1, __fmul_rn(sx, __ldg(p.ws + n + 8)));
+    if (p.out) p.out[at + 8] = __float2bfloat16_rn(u);
+    if (p.out_f32) p.out_f32[at + 8] = u;
   }
-  const int64_t at = (int64_t)t * p.NO + n;
   if (p.out) p.out[at] = __float2bfloat16_rn(v);
   if (p.out_f32) p.out_f32[at] = v;
 }
@@ -731,16 +748,10 @@ cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, 
   return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
 }
 
-template <int NT, bool GATED>
-cudaError_t launch_few(const LinParams& p, const int8_t* x, const int8_t* w, int K,
+template <int NB, bool GATED, int W>
+cudaError_t launch_few(const LinParams& p, int blocks, const int8_t* x, const int8_t* w, int K,
                        cudaStream_t st) {
-  // two rows per warp spread a small weight over every SM; four share each
-  // x vector between more rows once there are enough
-  const bool four = p.N >= 4 * 16 * device_sm_count();
-  const int rows = four ? 4 : 2;
-  const int blocks = ceil_div(p.NO, 4 * (GATED ? rows / 2 : rows));
-  auto kern = four ? linear_i8_few_kernel<NT, 4, GATED> : linear_i8_few_kernel<NT, 2, GATED>;
-  return launch_ex(kern, dim3(blocks), dim3(128), 0, st, true,
+  return launch_ex(linear_i8_few_kernel<NB, GATED, W>, dim3(blocks), dim3(32 * W), 0, st, true,
                    reinterpret_cast<const int4*>(x), reinterpret_cast<const int4*>(w), K / 16, p);
 }
 
@@ -788,10 +799,17 @@ template <bool GATED>
 cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cudaStream_t st) {
   const int sms = device_sm_count();
   const int rows = GATED ? 64 : 128;  // output channels of 128 weight rows
-  if (p.T <= 1) return launch_few<1, GATED>(p, x, w, K, st);
-  if (p.T <= 2) return launch_few<2, GATED>(p, x, w, K, st);
-  if (p.T <= 4) return launch_few<4, GATED>(p, x, w, K, st);
-  if (p.T <= 8) return launch_few<8, GATED>(p, x, w, K, st);
+  // Sixteen warps to a block while three blocks or fewer come to an SM, so that
+  // enough loads are in flight (gated 2816 x 4224, T = 1: 3.6 us, with eight 5.6;
+  // 4096 x 28672: 25.9 us, with eight 20.2).  A second tile of tokens pays for small
+  // weights alone, since every block reads all tokens (2816 x 4224, T = 16: 5.1 us
+  // against 6.3 on the tcgen05 form; 4096 x 14336: 19 against 13.7; 14336 x 4096: 17.1
+  // against 14.1).
+  const int blocks = ceil_div(p.NO, GATED ? 8 : 16);
+  if (p.T <= 8)
+    return blocks <= 3 * sms ? launch_few<1, GATED, 16>(p, blocks, x, w, K, st)
+                             : launch_few<1, GATED, 8>(p, blocks, x, w, K, st);
+  if (p.T <= 16 && blocks <= 2 * sms && K <= 4096) return launch_few<2, GATED, 16>(p, blocks, x, w, K, st);
   p.KB = ceil_div(K, 128);
   const int mt128 = ceil_div(p.NO, rows);
   if (p.T <= 128) {
