@@ -52,35 +52,83 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 
-__device__ __forceinline__ double squares(const float (&f)[8]) {
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s += (double)f[i] * (double)f[i];
-  return s;
+// A bf16 value's magnitude as a double, from its 15 bits moved to the upper word
+// (the lower one is zero): a shift and an add, where the conversion instruction
+// runs at an eighth of their rate.  Zeros and subnormals come out as up to
+// 2^-126 instead, whose squares vanish next to anything that fp32 can hold;
+// infinity and NaN as 2^128 and more, which block_squares catches.
+__device__ __forceinline__ double magnitude(uint32_t bits15) {
+  return __hiloint2double((int)(bits15 + 0x38000000u), 0);
 }
 
-// Sum over the block; red holds one value per warp.
+__device__ __forceinline__ double squares(const uint4& v) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  double s = 0.0, t = 0.0;  // two chains
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const double lo = magnitude((u[i] & 0x7fffu) << 13), hi = magnitude((u[i] & 0x7fff0000u) >> 3);
+    s = fma(lo, lo, s);
+    t = fma(hi, hi, t);
+  }
+  return s + t;
+}
+
+// The largest magnitude of eight bf16 values as its 15 bits, which order like the
+// values, with infinity and then NaN above them.
+__device__ __forceinline__ uint32_t abs_bits(const uint4& v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+
+// Sum and maximum over the block, for every thread; red holds one value per warp
+// and is not used again, so one barrier does.
 __device__ __forceinline__ double block_sum(double v, double* red) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
-  __syncthreads();  // red may still be read by the previous call
+  if (n == 1) return v;
   if (lane == 0) red[warp] = v;
   __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < n; ++i) s += red[i];
-  return s;
+  if (n <= 4) {
+    v = red[0] + red[1];
+    if (n > 2) v += red[2];
+    if (n > 3) v += red[3];
+    return v;
+  }
+  v = lane < n ? red[lane] : 0.0;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
 }
 
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
   v = __reduce_max_sync(0xffffffffu, v);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
-  __syncthreads();
+  if (n == 1) return v;
   if (lane == 0) red[warp] = v;
   __syncthreads();
-  uint32_t m = 0;
-  for (int i = 0; i < n; ++i) m = max(m, red[i]);
-  return m;
+  return __reduce_max_sync(0xffffffffu, lane < n ? red[lane] : 0u);
+}
+
+// Sum of the row's squares over the block, from this thread's vectors.  A sum of
+// 2^255 or more may hold infinities or NaN: then (a branch of the whole block) the
+// largest magnitude tells.
+template <int VPT>
+__device__ __forceinline__ double block_squares(const uint4 (&v)[VPT], double* red,
+                                                uint32_t* redm) {
+  double ss = 0.0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) ss += squares(v[j]);
+  ss = block_sum(ss, red);
+  if (ss >= 5.7896044618658098e76) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) m = max(m, abs_bits(v[j]));
+    m = block_max(m, redm);
+    if (m >= 0x7f80u) ss = (double)__uint_as_float(m << 16);  // infinity or NaN
+  }
+  return ss;
 }
 
 // 1 / sqrt(mean + eps), IEEE fp32, of the mean of squares rounded to fp32
@@ -88,25 +136,37 @@ __device__ __forceinline__ float rms_inverse(double ss, int H, float eps) {
   return 1.0f / sqrtf((float)(ss / (double)H) + eps);
 }
 
-// Largest |value| of eight bf16 values as their 15-bit patterns, which order
-// like the values, with infinity and then NaN above them.
-__device__ __forceinline__ uint32_t abs_bits(const uint4& v) {
-  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-  return max(m & 0xffffu, m >> 16);
-}
-
-__device__ __forceinline__ uint32_t code(float v, float s) {
-  // an infinite or NaN row (s not finite) gives v / s = 0 or NaN: code 0
-  const int c = __float2int_rn(__fdiv_rn(v, s));
-  return (uint32_t)max(-127, min(127, c)) & 0xffu;
+// rint(fl(v / s)) of eight values, as bytes.  inv is 1 / s rounded, or 0 where s is
+// outside [2^-60, 2^60] or not finite.  v inv is within 2.3e-5 of fl(v / s) (three
+// roundings of 2^-24 of at most 127), so it has the same nearest integer unless
+// it comes that near to a half; those, and every row without inv, divide.  Adding
+// 1.5 2^23 rounds to an integer in the low bits.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float s, float inv) {
+  uint32_t c[8];
+  float off = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = __fmul_rn(f[i], inv);
+    const float r = __fadd_rn(t, 12582912.0f);
+    c[i] = __float_as_uint(r);
+    off = fmaxf(off, fabsf(__fsub_rn(t, __fsub_rn(r, 12582912.0f))));
+  }
+  if (off > 0.49993896f || inv == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // a row that is not finite: 0 or NaN, code 0
+      c[i] = (uint32_t)max(-127, min(127, __float2int_rn(__fdiv_rn(f[i], s))));
+  }
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+  return o;
 }
 
 template <int VPT>
 __global__ void __launch_bounds__(1024)
 rows_kernel(const RowParams p) {
-  __shared__ double red[32];
-  __shared__ uint32_t redm[32];
+  __shared__ double red[2][32];
+  __shared__ uint32_t redm[3][32];
   pdl_wait();
   pdl_trigger();
   const int64_t t = blockIdx.x, base = t * p.vec;
@@ -126,14 +186,7 @@ rows_kernel(const RowParams p) {
     }
     float inv = 1.0f;
     if (p.post_w) {
-      double ss = 0.0;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        float f[8];
-        unpack8(y[j], f);
-        ss += squares(f);
-      }
-      inv = rms_inverse(block_sum(ss, red), p.H, p.post_eps);
+      inv = rms_inverse(block_squares<VPT>(y, red[0], redm[0]), p.H, p.post_eps);
     }
     const float m = p.token_gate ? __fmul_rn(p.beta, p.token_gate[t]) : p.beta;
 #pragma unroll
@@ -162,14 +215,7 @@ rows_kernel(const RowParams p) {
     }
   }
   if (p.pre_w) {
-    double ss = 0.0;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      float f[8];
-      unpack8(r[j], f);
-      ss += squares(f);
-    }
-    const float inv = rms_inverse(block_sum(ss, red), p.H, p.pre_eps);
+    const float inv = rms_inverse(block_squares<VPT>(r, red[1], redm[1]), p.H, p.pre_eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = tid + j * nt;
@@ -188,18 +234,16 @@ rows_kernel(const RowParams p) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) m = max(m, abs_bits(r[j]));
-    const float amax = __uint_as_float(block_max(m, redm) << 16);
+    const float amax = __uint_as_float(block_max(m, redm[2]) << 16);
     const float s = amax == 0.0f ? 1.0f : __fdiv_rn(amax, 127.0f);
+    const float inv = s >= 8.6736174e-19f && s <= 1.1529215e18f ? __frcp_rn(s) : 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = tid + j * nt;
       if (c < p.vec) {
         float f[8];
         unpack8(r[j], f);
-        uint2 o;
-        o.x = code(f[0], s) | code(f[1], s) << 8 | code(f[2], s) << 16 | code(f[3], s) << 24;
-        o.y = code(f[4], s) | code(f[5], s) << 8 | code(f[6], s) << 16 | code(f[7], s) << 24;
-        p.codes[base + c] = o;
+        p.codes[base + c] = codes8(f, s, inv);
       }
     }
     if (tid == 0) p.scales[t] = s;
@@ -207,11 +251,14 @@ rows_kernel(const RowParams p) {
 }
 
 cudaError_t launch_rows(int64_t rows, const RowParams& p, cudaStream_t st) {
-  const int vpt = p.vec <= 128 ? 1 : p.vec <= 256 ? 2 : 4;
-  int nt = (p.vec + vpt - 1) / vpt;
-  nt = (nt + 31) / 32 * 32;
-  auto kern = vpt == 1 ? rows_kernel<1> : vpt == 2 ? rows_kernel<2> : rows_kernel<4>;
-  return launch_ex(kern, dim3((unsigned)rows), dim3(nt), 0, st, false, p);
+  // few rows: as many threads as the row has vectors; many: a few warps per row,
+  // several vectors to a thread
+  int vpt = rows <= 2 * device_sm_count() ? 1 : (p.vec + 127) / 128;
+  while (vpt < 4 && p.vec > vpt * 1024) ++vpt;
+  vpt = vpt < 4 ? vpt : 4;
+  const int nt = ((p.vec + vpt - 1) / vpt + 31) / 32 * 32;
+  auto kern = vpt == 1 ? rows_kernel<1> : vpt == 2 ? rows_kernel<2> : vpt == 3 ? rows_kernel<3> : rows_kernel<4>;
+  return launch_ex(kern, dim3((unsigned)rows), dim3(nt), 0, st, true, p);
 }
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
