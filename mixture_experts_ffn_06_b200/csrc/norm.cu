@@ -9,13 +9,13 @@
 //
 // Bound: HBM.  A row is read once and kept in registers (8 bf16 values per
 // 16-byte vector, VPT vectors per thread) through its up to three reductions,
-// so every input byte is read once and every output byte written once.  One
-// block per row.
+// so every input byte is read once and every output byte written once.
 //
 // The means are taken in double (a square of a bf16 value is exact in fp32),
 // so that they round to the same fp32 value whatever the order of the sum, and
 // with IEEE divisions and square roots the rows and their codes come out the
 // same bits as the steps taken one by one.
+#include <algorithm>
 #include <cmath>
 
 #include "internal.cuh"
@@ -30,45 +30,53 @@ struct RowParams {
   uint4 *r_out, *a;
   uint2* codes;
   float* scales;
-  int vec;  // 16-byte vectors per row
-  int H;
+  int64_t rows;
+  int vec;        // 16-byte vectors per row
+  double n, inv_n;  // values per row, 1 / n
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// Two fp32 operations at once, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  uint32_t u[4];
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
+    u[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-}
-
-// A bf16 value's magnitude as a double, from its 15 bits moved to the upper word
-// (the lower one is zero): a shift and an add, where the conversion instruction
-// runs at an eighth of their rate.  Zeros and subnormals come out as up to
-// 2^-126 instead, whose squares vanish next to anything that fp32 can hold;
-// infinity and NaN as 2^128 and more, which block_squares catches.
-__device__ __forceinline__ double magnitude(uint32_t bits15) {
-  return __hiloint2double((int)(bits15 + 0x38000000u), 0);
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 __device__ __forceinline__ double squares(const uint4& v) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  float2 f[4];
+  unpack8(v, f);
   double s = 0.0, t = 0.0;  // two chains
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const double lo = magnitude((u[i] & 0x7fffu) << 13), hi = magnitude((u[i] & 0x7fff0000u) >> 3);
-    s = fma(lo, lo, s);
-    t = fma(hi, hi, t);
+    s = fma((double)f[i].x, (double)f[i].x, s);
+    t = fma((double)f[i].y, (double)f[i].y, t);
   }
   return s + t;
 }
@@ -111,29 +119,22 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
   return __reduce_max_sync(0xffffffffu, lane < n ? red[lane] : 0u);
 }
 
-// Sum of the row's squares over the block, from this thread's vectors.  A sum of
-// 2^255 or more may hold infinities or NaN: then (a branch of the whole block) the
-// largest magnitude tells.
+// Sum of the row's squares over the block, from this thread's vectors.
 template <int VPT>
-__device__ __forceinline__ double block_squares(const uint4 (&v)[VPT], double* red,
-                                                uint32_t* redm) {
+__device__ __forceinline__ double block_squares(const uint4 (&v)[VPT], double* red) {
   double ss = 0.0;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) ss += squares(v[j]);
-  ss = block_sum(ss, red);
-  if (ss >= 5.7896044618658098e76) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) m = max(m, abs_bits(v[j]));
-    m = block_max(m, redm);
-    if (m >= 0x7f80u) ss = (double)__uint_as_float(m << 16);  // infinity or NaN
-  }
-  return ss;
+  return block_sum(ss, red);
 }
 
-// 1 / sqrt(mean + eps), IEEE fp32, of the mean of squares rounded to fp32
-__device__ __forceinline__ float rms_inverse(double ss, int H, float eps) {
-  return 1.0f / sqrtf((float)(ss / (double)H) + eps);
+// 1 / sqrt(mean + eps), IEEE fp32, of the mean of squares rounded to fp32.  The
+// quotient in double by its reciprocal and one exact remainder: right to the last
+// bit wherever it can lie halfway between two fp32 values.
+__device__ __forceinline__ float rms_inverse(double ss, const RowParams& p, float eps) {
+  double q = ss * p.inv_n;
+  if (q < 1e300) q = fma(fma(-q, p.n, ss), p.inv_n, q);
+  return 1.0f / sqrtf((float)q + eps);
 }
 
 // rint(fl(v / s)) of eight values, as bytes.  inv is 1 / s rounded, or 0 where s is
@@ -141,20 +142,25 @@ __device__ __forceinline__ float rms_inverse(double ss, int H, float eps) {
 // roundings of 2^-24 of at most 127), so it has the same nearest integer unless
 // it comes that near to a half; those, and every row without inv, divide.  Adding
 // 1.5 2^23 rounds to an integer in the low bits.
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float s, float inv) {
+__device__ __forceinline__ uint2 codes8(const float2 (&f)[4], float s, float inv) {
   uint32_t c[8];
   float off = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __fmul_rn(f[i], inv);
-    const float r = __fadd_rn(t, 12582912.0f);
-    c[i] = __float_as_uint(r);
-    off = fmaxf(off, fabsf(__fsub_rn(t, __fsub_rn(r, 12582912.0f))));
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = mul2(f[i], both(inv));
+    const float2 r = add2(t, both(12582912.0f));
+    // t - (r - 1.5 2^23), both exact
+    const float2 d = add2(add2(r, both(-12582912.0f)), make_float2(-t.x, -t.y));
+    c[2 * i] = __float_as_uint(r.x);
+    c[2 * i + 1] = __float_as_uint(r.y);
+    off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
   }
   if (off > 0.49993896f || inv == 0.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // a row that is not finite: 0 or NaN, code 0
-      c[i] = (uint32_t)max(-127, min(127, __float2int_rn(__fdiv_rn(f[i], s))));
+    for (int i = 0; i < 8; ++i) {  // a row that is not finite: 0 or NaN, code 0
+      const float v = (i & 1) ? f[i / 2].y : f[i / 2].x;
+      c[i] = (uint32_t)max(-127, min(127, __float2int_rn(__fdiv_rn(v, s))));
+    }
   }
   uint2 o;
   o.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
@@ -166,65 +172,60 @@ template <int VPT>
 __global__ void __launch_bounds__(1024)
 rows_kernel(const RowParams p) {
   __shared__ double red[2][32];
-  __shared__ uint32_t redm[3][32];
+  __shared__ uint32_t redm[32];
   pdl_wait();
   pdl_trigger();
-  const int64_t t = blockIdx.x, base = t * p.vec;
+  // (blockDim.y rows to a block only where a row is one warp's: no barrier then)
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, base = t * p.vec;
+  if (t >= p.rows) return;
   const int tid = threadIdx.x, nt = blockDim.x;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4 r[VPT];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = tid + j * nt;
-    r[j] = c < p.vec ? p.r[base + c] : make_uint4(0, 0, 0, 0);
-  }
+  for (int j = 0; j < VPT; ++j) r[j] = tid + j * nt < p.vec ? p.r[base + tid + j * nt] : zero;
   if (p.y) {
     uint4 y[VPT];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = tid + j * nt;
-      y[j] = c < p.vec ? p.y[base + c] : make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < VPT; ++j) y[j] = tid + j * nt < p.vec ? p.y[base + tid + j * nt] : zero;
     float inv = 1.0f;
-    if (p.post_w) {
-      inv = rms_inverse(block_squares<VPT>(y, red[0], redm[0]), p.H, p.post_eps);
-    }
+    if (p.post_w) inv = rms_inverse(block_squares<VPT>(y, red[0]), p, p.post_eps);
     const float m = p.token_gate ? __fmul_rn(p.beta, p.token_gate[t]) : p.beta;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = tid + j * nt;
       if (c < p.vec) {
-        float f[8], g[8], o[8];
+        float2 f[4], g[4], o[4];
         unpack8(y[j], f);
         if (p.post_w) {
           unpack8(__ldg(p.post_w + c), g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(f[i], inv), g[i]);
+          for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], both(inv)), g[i]);
         }
         if (p.gate) {
           unpack8(__ldg(p.gate + c), g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], g[i]);
+          for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], g[i]);
         }
         unpack8(r[j], o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i] = __fadd_rn(__fmul_rn(p.alpha, o[i]), __fmul_rn(m, f[i]));
+        for (int i = 0; i < 4; ++i)
+          o[i] = add2(mul2(both(p.alpha), o[i]), mul2(both(m), f[i]));
         r[j] = pack8(o);
         p.r_out[base + c] = r[j];
       }
     }
   }
   if (p.pre_w) {
-    const float inv = rms_inverse(block_squares<VPT>(r, red[1], redm[1]), p.H, p.pre_eps);
+    const float inv = rms_inverse(block_squares<VPT>(r, red[1]), p, p.pre_eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = tid + j * nt;
       if (c < p.vec) {
-        float f[8], g[8];
+        float2 f[4], g[4];
         unpack8(r[j], f);
         unpack8(__ldg(p.pre_w + c), g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(f[i], inv), g[i]);
+        for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], both(inv)), g[i]);
         r[j] = pack8(f);
         if (p.a) p.a[base + c] = r[j];
       }
@@ -234,14 +235,14 @@ rows_kernel(const RowParams p) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) m = max(m, abs_bits(r[j]));
-    const float amax = __uint_as_float(block_max(m, redm[2]) << 16);
+    const float amax = __uint_as_float(block_max(m, redm) << 16);
     const float s = amax == 0.0f ? 1.0f : __fdiv_rn(amax, 127.0f);
     const float inv = s >= 8.6736174e-19f && s <= 1.1529215e18f ? __frcp_rn(s) : 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = tid + j * nt;
       if (c < p.vec) {
-        float f[8];
+        float2 f[4];
         unpack8(r[j], f);
         p.codes[base + c] = codes8(f, s, inv);
       }
@@ -250,15 +251,27 @@ rows_kernel(const RowParams p) {
   }
 }
 
-cudaError_t launch_rows(int64_t rows, const RowParams& p, cudaStream_t st) {
-  // few rows: as many threads as the row has vectors; many: a few warps per row,
-  // several vectors to a thread
-  int vpt = rows <= 2 * device_sm_count() ? 1 : (p.vec + 127) / 128;
-  while (vpt < 4 && p.vec > vpt * 1024) ++vpt;
-  vpt = vpt < 4 ? vpt : 4;
-  const int nt = ((p.vec + vpt - 1) / vpt + 31) / 32 * 32;
-  auto kern = vpt == 1 ? rows_kernel<1> : vpt == 2 ? rows_kernel<2> : vpt == 3 ? rows_kernel<3> : rows_kernel<4>;
-  return launch_ex(kern, dim3((unsigned)rows), dim3(nt), 0, st, true, p);
+cudaError_t launch_rows(int64_t rows, RowParams& p, cudaStream_t st) {
+  p.rows = rows;
+  // Few rows: a thread per vector.  Many: three or four vectors per thread, which
+  // shares a row's fixed cost (two means, two inverse roots) between them and still
+  // leaves enough rows on an SM (T = 8192, H = 4096, both norms: 47.5 us with 128
+  // threads, 54.3 with 96, 52.5 with 256, 65.2 with 512; H = 2816: 35.6 us with three
+  // on 128 threads, 36.3 with four on 96).  A row of up to 1024
+  // values is one warp's; then eight of them share a block.
+  int nt = std::min(1024, (p.vec + 31) / 32 * 32), per = 1;
+  if (rows > 2 * device_sm_count()) {
+    nt = (p.vec + 127) / 128 * 32;
+    const int nt3 = (p.vec + 95) / 96 * 32;
+    if (3 * nt3 <= 4 * nt) nt = nt3;
+    if (p.vec <= 128) nt = 32, per = 8;
+  }
+  const int vpt = (p.vec + nt - 1) / nt;
+  auto kern = vpt == 1   ? rows_kernel<1>
+              : vpt == 2 ? rows_kernel<2>
+              : vpt == 3 ? rows_kernel<3>
+                         : rows_kernel<4>;
+  return launch_ex(kern, dim3((unsigned)((rows + per - 1) / per)), dim3(nt, per), 0, st, true, p);
 }
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -282,7 +295,8 @@ moe_status moe_quantize_rows_i8(const moe_bf16* src, int64_t rows, int cols, int
   p.codes = reinterpret_cast<uint2*>(codes);
   p.scales = scales;
   p.vec = cols / 8;
-  p.H = cols;
+  p.n = cols;
+  p.inv_n = 1.0 / cols;
   return launch_rows(rows, p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -323,7 +337,8 @@ moe_status moe_block_norm(int64_t T, int H, const moe_block_norm_params* q,
   p.codes = reinterpret_cast<uint2*>(q->codes);
   p.scales = q->scales;
   p.vec = H / 8;
-  p.H = H;
+  p.n = H;
+  p.inv_n = 1.0 / H;
   return launch_rows(T, p, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
