@@ -4,9 +4,18 @@
 // group_top largest c sum highest, the k largest c inside them, weights from
 // the s of the chosen.
 //
-// A warp per token; lane l holds experts l, l + 32, ... (PER per lane).  The
-// choice is made on fp64 values, so that it is the one the definition gives
-// and not one of an fp32 rounding; equal values go to the lower id.
+// The definition ranks c in 64 bits.  Here c is formed in fp32 with a bound on its
+// error, and the choice is taken as made only where every gap it rests on (between
+// consecutive chosen values, to the runner-up, between groups) is wider than
+// that bound; the few tokens where one is not are chosen again on fp64 values
+// (exact_choice).  The weights of the k chosen are fp64 throughout.
+//
+// LT lanes take a token (8 where there are many tokens, a whole warp where there
+// are few), each lane PER experts of one group: it sorts its values, packed with
+// their place in the low bits, by a network, so that a round of the top-k is a
+// maximum over the LT heads, and a group of one lane has its two largest in
+// front.  Bound by the instructions per expert (score and sort), then by
+// the k rounds; the bytes (4 E + 8 k per token) would take a tenth of the time.
 #include <cfloat>
 #include <cmath>
 
@@ -40,6 +49,10 @@ __device__ __forceinline__ unsigned long long warp_max64(unsigned long long v) {
 __device__ __forceinline__ float clamp_logit(float z) { return z > FLT_MAX ? FLT_MAX : z; }
 __device__ __forceinline__ bool available(float z) { return z > -INFINITY; }
 
+__device__ __forceinline__ double value64(unsigned long long k) {
+  return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
+
 __device__ __forceinline__ double score64(float z, float zmax, double inv, bool sigmoid) {
   if (!available(z)) return 0.0;
   return sigmoid ? 1.0 / (1.0 + exp(-(double)z)) : exp((double)z - (double)zmax) * inv;
@@ -52,140 +65,510 @@ __device__ __forceinline__ double choice64(float z, double s, float b) {
   return c == c ? fmin(c, DBL_MAX) : -INFINITY;
 }
 
-template <int PER>
-__global__ void __launch_bounds__(256)
+// 1 / sum of exp(z - zmax) over a row, by the whole warp.
+__device__ __forceinline__ double softmax_inverse64(const float* __restrict__ zr, int E,
+                                                    float zmax) {
+  double sum = 0.0;
+  for (int e = threadIdx.x & 31; e < E; e += 32)
+    sum += score64(clamp_logit(__ldg(zr + e)), zmax, 1.0, false);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  return 1.0 / sum;
+}
+
+// Puts n <= 32 candidates of a token in the order of their fp64 values (equal ones
+// by id), by the whole warp: each lane forms one and counts those before it.
+__device__ __noinline__ void rank_exactly(const float* __restrict__ zr,
+                                          const float* __restrict__ bias, int E, float zmax,
+                                          bool sigmoid, int n, int16_t* list) {
+  const int lane = threadIdx.x & 31;
+  const double inv = sigmoid ? 1.0 : softmax_inverse64(zr, E, zmax);
+  const int id = lane < n ? list[lane] : E;
+  double c = -INFINITY;
+  if (lane < n) {
+    const float z = clamp_logit(__ldg(zr + id));
+    c = choice64(z, score64(z, zmax, inv, sigmoid), bias ? __ldg(bias + id) : 0.f);
+  }
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const double ci = __shfl_sync(kAll, c, i);
+    const int idi = __shfl_sync(kAll, id, i);
+    rank += ci > c || (ci == c && idi < id);
+  }
+  __syncwarp();  // every lane has read its entry
+  if (lane < n) list[rank] = (int16_t)id;
+}
+
+// The k chosen experts of one token on fp64 values alone, by the whole warp: rounds
+// of a maximum over key[E], ordered keys in shared memory (0: not a candidate),
+// equal values to the lower id.
+__device__ __noinline__ void exact_choice(const float* __restrict__ zr,
+                                          const float* __restrict__ bias, int E, int k,
+                                          float zmax, const BalanceOpt& o,
+                                          unsigned long long* key, int16_t* out) {
+  const int lane = threadIdx.x & 31;
+  const bool sigmoid = o.scoring == MOE_SCORE_SIGMOID;
+  const double inv = sigmoid ? 1.0 : softmax_inverse64(zr, E, zmax);
+  for (int e = lane; e < E; e += 32) {
+    const float z = clamp_logit(__ldg(zr + e));
+    key[e] = key64(choice64(z, score64(z, zmax, inv, sigmoid), bias ? __ldg(bias + e) : 0.f));
+  }
+  __syncwarp();
+  // the largest key of [e0, e1) and the lowest id that has it; takes it out
+  auto take = [&](int e0, int e1, int* win) {
+    unsigned long long best = 0;
+    uint32_t at = kAll;
+    for (int e = e0 + lane; e < e1; e += 32)
+      if (key[e] > best) {
+        best = key[e];
+        at = (uint32_t)e;
+      }
+    const unsigned long long top = warp_max64(best);
+    *win = (int)__reduce_min_sync(kAll, best == top ? at : kAll);
+    return top;
+  };
+  if (o.n_group > 1) {
+    const int gs = E / o.n_group;
+    unsigned long long mine = 0;  // lane g: group g's score
+    for (int g = 0; g < o.n_group; ++g) {
+      int win;
+      const unsigned long long top = take(g * gs, g * gs + gs, &win);
+      double sum = value64(top);
+      if (o.group_top == 2 && gs > 1) {
+        __syncwarp();
+        if (lane == 0) key[win] = 0;
+        __syncwarp();
+        int unused;
+        sum += value64(take(g * gs, g * gs + gs, &unused));
+        __syncwarp();
+        if (lane == 0) key[win] = top;
+        __syncwarp();
+      }
+      if (lane == g) mine = key64(sum);
+    }
+    uint32_t keep = 0;
+    for (int r = 0; r < o.topk_group; ++r) {
+      const unsigned long long top = warp_max64(mine);
+      const int win = __ffs(__ballot_sync(kAll, mine == top)) - 1;
+      keep |= 1u << win;
+      if (lane == win) mine = 0;
+    }
+    for (int e = lane; e < E; e += 32)
+      if (!((keep >> (e / gs)) & 1u)) key[e] = 0;
+    __syncwarp();
+  }
+  for (int j = 0; j < k; ++j) {
+    int win;
+    take(0, E, &win);
+    __syncwarp();
+    if (lane == 0) {
+      key[win] = 0;
+      out[j] = (int16_t)win;
+    }
+    __syncwarp();
+  }
+}
+
+// ---- sorting networks on packed keys, largest first
+
+template <int N, int I, int J>
+__device__ __forceinline__ void cas(uint32_t (&a)[N]) {
+  const uint32_t hi = max(a[I], a[J]), lo = min(a[I], a[J]);
+  a[I] = hi;
+  a[J] = lo;
+}
+
+// Bitonic network: sorts a[B, B + S) whose first half falls and second half rises.
+template <int N, int B, int S>
+__device__ __forceinline__ void merge(uint32_t (&a)[N]) {
+  if constexpr (S > 1) {
+#pragma unroll
+    for (int i = B; i < B + S / 2; ++i) {
+      const uint32_t hi = max(a[i], a[i + S / 2]), lo = min(a[i], a[i + S / 2]);
+      a[i] = hi;
+      a[i + S / 2] = lo;
+    }
+    merge<N, B, S / 2>(a);
+    merge<N, B + S / 2, S / 2>(a);
+  }
+}
+
+template <int N, int B, int S>
+__device__ __forceinline__ void sort(uint32_t (&a)[N]) {
+  if constexpr (S == 8) {  // odd-even merge sort: 19 exchanges, the bitonic one has 24
+    cas<N, B, B + 1>(a); cas<N, B + 2, B + 3>(a); cas<N, B + 4, B + 5>(a); cas<N, B + 6, B + 7>(a);
+    cas<N, B, B + 2>(a); cas<N, B + 1, B + 3>(a); cas<N, B + 4, B + 6>(a); cas<N, B + 5, B + 7>(a);
+    cas<N, B + 1, B + 2>(a); cas<N, B + 5, B + 6>(a);
+    cas<N, B, B + 4>(a); cas<N, B + 1, B + 5>(a); cas<N, B + 2, B + 6>(a); cas<N, B + 3, B + 7>(a);
+    cas<N, B + 2, B + 4>(a); cas<N, B + 3, B + 5>(a);
+    cas<N, B + 1, B + 2>(a); cas<N, B + 3, B + 4>(a); cas<N, B + 5, B + 6>(a);
+  } else if constexpr (S > 1) {
+    sort<N, B, S / 2>(a);
+    sort<N, B + S / 2, S / 2>(a);
+    // turn the second half round: falling, then rising
+    if constexpr (S > 2) {
+#pragma unroll
+      for (int i = 0; i < S / 4; ++i) {
+        const uint32_t t = a[B + S / 2 + i];
+        a[B + S / 2 + i] = a[B + S - 1 - i];
+        a[B + S - 1 - i] = t;
+      }
+    }
+    merge<N, B, S>(a);
+  }
+}
+
+// The eight largest of a (runs of eight), sorted, in a[0, 8).
+template <int N>
+__device__ __forceinline__ void top8(uint32_t (&a)[N]) {
+  if constexpr (N <= 8) {
+    sort<N, 0, N>(a);
+  } else {
+    sort<N, 0, 8>(a);
+    sort<N, 8, 8>(a);
+    if constexpr (N == 32) {
+      sort<N, 16, 8>(a);
+      sort<N, 24, 8>(a);
+    }
+    // the larger of the i-th and the (7 - i)-th of two runs are their eight largest
+#pragma unroll
+    for (int h = 0; h < N; h += 16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[h + i] = max(a[h + i], a[h + 15 - i]);
+    }
+    merge<N, 0, 8>(a);
+    if constexpr (N == 32) {
+      merge<N, 16, 8>(a);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = max(a[i], a[23 - i]);
+      merge<N, 0, 8>(a);
+    }
+  }
+}
+
+template <int LT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
+  if constexpr (LT == 32) {
+    v = __reduce_max_sync(kAll, v);
+  } else {
+#pragma unroll
+    for (int off = LT / 2; off > 0; off >>= 1) v = max(v, __shfl_xor_sync(kAll, v, off));
+  }
+  return v;
+}
+
+template <int LT>
+__device__ __forceinline__ float token_max(float v) {
+#pragma unroll
+  for (int off = LT / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+  return v;
+}
+
+template <int LT>
+__device__ __forceinline__ double token_sum(double v) {
+#pragma unroll
+  for (int off = LT / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  return v;
+}
+
+// Experts of a lane.  The LT lanes of a token are dealt to the groups, ``lanes``
+// (a power of two) each; a lane's i-th expert is i * lanes + sub places into its
+// group, or with quads four at a time, read as 16-byte vectors.
+struct Deal {
+  int groups, size;  // 1 and E without groups
+  int lanes;         // lanes per group
+  int n;             // experts per lane, at most
+  int quads;
+};
+
+constexpr int kRouteWarps = 16;
+
+// c of an expert as the choice compares it, in fp32.
+__device__ __forceinline__ float choice32(float term, float inv, float b, bool sigmoid) {
+  const float c = (sigmoid ? __fdividef(1.0f, 1.0f + __expf(-term)) : term * inv) + b;
+  return available(term) && c == c ? c : -INFINITY;
+}
+
+template <int LT, int PER, bool K8>  // K8: k <= 8
+__global__ void __launch_bounds__(32 * kRouteWarps, PER <= 8 ? 2 : 1)
 balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
                const float* __restrict__ scale, int64_t T, int E, int k,
                int32_t* __restrict__ ids, float* __restrict__ w, int32_t* __restrict__ load,
-               const BalanceOpt o) {
-  extern __shared__ int32_t hist[];  // [E] when load is given
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
-  pdl_trigger();
+               const BalanceOpt o, const Deal d) {
+  constexpr int TW = 32 / LT;                // tokens per warp
+  constexpr uint32_t LOW = PER - 1;          // place of an expert in its lane, reversed
+  constexpr int M = K8 && PER > 8 ? 8 : PER;  // sorted entries a lane keeps
+  constexpr int LIST = K8 ? 16 : 32;         // candidates of a token, at most
+  extern __shared__ unsigned long long keys_s[];  // [warps][E], exact_choice's
+  __shared__ int hist[kMaxExperts];
+  __shared__ int16_t list_s[kRouteWarps][TW][LIST];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int tl = lane % LT, tw = lane / LT;
+  const uint32_t mask = LT == 32 ? kAll : ((1u << LT) - 1u) << (tw * LT);  // this token's lanes
+  const bool sigmoid = o.scoring == MOE_SCORE_SIGMOID;
+  const int g = tl / d.lanes, sub = tl % d.lanes;  // this lane's group and place in it
+  const bool in = g < d.groups;
+  // its first expert, and how many it has
+  const int e0 = g * d.size + (d.quads ? 4 * sub : sub);
+  int nv = 0;
+  if (in)
+    nv = d.quads ? 4 * ((d.size - 4 * sub + 4 * d.lanes - 1) / (4 * d.lanes))
+                 : (d.size - sub + d.lanes - 1) / d.lanes;
+  const int step = d.quads ? 4 * d.lanes : d.lanes;
+  auto expert = [&](int i) { return d.quads ? e0 + (i >> 2) * step + (i & 3) : e0 + i * step; };
+  int16_t* list = list_s[warp][tw];
   if (load) {
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
   }
-  const bool sigmoid = o.scoring == MOE_SCORE_SIGMOID;
-  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-  if (t < T) {
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t base = ((int64_t)blockIdx.x * warps + warp) * TW; base < T;
+       base += (int64_t)gridDim.x * warps * TW) {
+    // lanes past the last token route it once more and store nothing
+    const int64_t t = base + tw < T ? base + tw : T - 1;
     const float* zr = logits + t * E;
     float z[PER];
     float zmax = -INFINITY;
+    bool quads = false;
+    if constexpr (PER >= 4) {
+      quads = d.quads;
+      if (quads) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      z[i] = e < E ? clamp_logit(__ldg(zr + e)) : -INFINITY;
-      if (available(z[i])) zmax = fmaxf(zmax, z[i]);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) zmax = fmaxf(zmax, __shfl_xor_sync(kAll, zmax, off));
-    double inv = 1.0;
-    if (!sigmoid) {
-      double sum = 0.0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) sum += score64(z[i], zmax, 1.0, false);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-      inv = 1.0 / sum;
-    }
-    double c[PER];
-    unsigned long long key[PER];  // 0: not a candidate
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      c[i] = e < E ? choice64(z[i], score64(z[i], zmax, inv, sigmoid), bias ? __ldg(bias + e) : 0.f)
-                   : -INFINITY;
-      key[i] = e < E ? key64(c[i]) : 0ull;
-    }
-    if (o.n_group > 1) {
-      const int gs = E / o.n_group;
-      // lane g gets group g's score
-      unsigned long long mine = 0;
-      for (int g = 0; g < o.n_group; ++g) {
-        unsigned long long best = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if ((lane + 32 * i) / gs == g) best = max(best, key[i]);
-        const unsigned long long top = warp_max64(best);
-        double sum = __longlong_as_double((top >> 63) ? top & 0x7fffffffffffffffull : ~top);
-        if (o.group_top == 2) {
-          // the second largest: drop one entry that holds the largest
-          uint32_t cand = kAll;
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E && e / gs == g && key[i] == top) cand = min(cand, (uint32_t)e);
-          }
-          const uint32_t drop = __reduce_min_sync(kAll, cand);
-          best = 0;
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E && e / gs == g && (uint32_t)e != drop) best = max(best, key[i]);
-          }
-          const unsigned long long second = warp_max64(best);
-          if (second)
-            sum += __longlong_as_double((second >> 63) ? second & 0x7fffffffffffffffull
-                                                       : ~second);
+        for (int i = 0; i < PER; i += 4) {
+          float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          if (i < nv) v = __ldg(reinterpret_cast<const float4*>(zr + e0 + (i >> 2) * step));
+          z[i] = v.x;
+          z[i + 1] = v.y;
+          z[i + 2] = v.z;
+          z[i + 3] = v.w;
         }
-        if (lane == g) mine = key64(sum);
       }
-      uint32_t keep = 0;
-      for (int r = 0; r < o.topk_group; ++r) {
-        const unsigned long long top = warp_max64(mine);
-        const int win = __ffs(__ballot_sync(kAll, mine == top)) - 1;
-        keep |= 1u << win;
-        if (lane == win) mine = 0;
-      }
+    }
+    if (!quads) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) z[i] = i < nv ? __ldg(zr + e0 + i * step) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      z[i] = clamp_logit(z[i]);
+      zmax = fmaxf(zmax, z[i]);  // a NaN is passed over
+    }
+    zmax = token_max<LT>(zmax);
+    // Scores.  The fp32 exponential is within |x| 2^-23 + 2^-22 of its value; with
+    // |x| e^-|x| < 0.37 a sigmoid is within 2^-21, and a softmax's term within
+    // 2^-21 of the largest.  Its denominator adds at most ln(512) 2^-23 + 2^-22 and
+    // 21 roundings: 2^-18 of the largest score in all.
+    float err = 9.5367432e-07f;  // 2^-20: two values
+    float inv = 1.0f;
+    double den = 0.0;
+    if (!sigmoid) {
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E && !((keep >> (e / gs)) & 1u)) key[i] = 0;
+        const bool a = available(z[i]);
+        if (!o.renorm && a) den += (double)expf(z[i] - zmax);
+        z[i] = a ? __expf(z[i] - zmax) : z[i];  // now the term, or -inf / NaN
+        sum += a ? z[i] : 0.0f;
+      }
+#pragma unroll
+      for (int s = LT / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(kAll, sum, s);
+      if (!o.renorm) den = token_sum<LT>(den);
+      inv = __fdividef(1.0f, sum);
+      err = 7.6293945e-06f * inv;  // 2^-17 of the largest score
+    }
+    uint32_t a[PER];
+    float v0 = -INFINITY, v1 = -INFINITY;  // this lane's two largest c (for its group)
+    auto pack = [&](int i, float b) {
+      const float c = choice32(z[i], inv, b, sigmoid);
+      if (d.groups > 1) {
+        const float u = i < nv ? c : -INFINITY;
+        v1 = fmaxf(v1, fminf(v0, u));
+        v0 = fmaxf(v0, u);
+      }
+      const uint32_t u = __float_as_uint(c);
+      const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+      a[i] = i < nv ? (key & ~LOW) | (LOW - i) : 0u;
+    };
+    if constexpr (PER >= 4) {
+      if (quads) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+          float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (bias && i < nv)
+            b = __ldg(reinterpret_cast<const float4*>(bias + e0 + (i >> 2) * step));
+          pack(i, b.x);
+          pack(i + 1, b.y);
+          pack(i + 2, b.z);
+          pack(i + 3, b.w);
+        }
       }
     }
-    int my_id = 0;
-    bool usable = false;  // c above -inf
-    for (int j = 0; j < k; ++j) {
-      unsigned long long best = 0;
+    if (!quads) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-      const unsigned long long top = warp_max64(best);
-      uint32_t cand = kAll;
+      for (int i = 0; i < PER; ++i) pack(i, bias && i < nv ? __ldg(bias + e0 + i * step) : 0.f);
+    }
+    if constexpr (K8)
+      top8<PER>(a);
+    else
+      sort<PER, 0, PER>(a);
+    auto value = [](uint32_t key) {
+      key &= ~LOW;
+      return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+    };
+    // a packed value is short of c by less than 2^-23 PER |c|; c itself rounds once
+    constexpr float REL = 2.0f * (PER + 1) * 1.1920929e-07f;
+    bool all_again = false;  // the whole choice has to be made on fp64 values
+    if (d.groups > 1) {
+      const bool two = o.group_top == 2 && d.size > 1;
+      for (int s = 1; s < d.lanes; s <<= 1) {
+        const float w0 = __shfl_xor_sync(kAll, v0, s), w1 = __shfl_xor_sync(kAll, v1, s);
+        v1 = fmaxf(fminf(v0, w0), fmaxf(v1, w1));
+        v0 = fmaxf(v0, w0);
+      }
+      const float score = two ? v0 + v1 : v0;
+      int rank = 0;
+      for (int s = d.lanes; s < LT; s += d.lanes) {
+        const float other = __shfl_xor_sync(kAll, score, s);
+        const int og = (tl ^ s) / d.lanes;
+        rank += og < d.groups && (other > score || (other == score && og < g));
+      }
+      const bool kept = in && rank < o.topk_group;
+      if (o.topk_group < d.groups) {
+        // the lowest kept score against the highest other
+        const float low = -token_max<LT>(kept ? -score : -INFINITY);
+        const float high = token_max<LT>(in && !kept ? score : -INFINITY);
+        const float mag = token_max<LT>(in ? fabsf(v0) + (two ? fabsf(v1) : 0.0f) : 0.0f);
+        all_again = !(low - high > 2.0f * err + 4.8e-07f * mag);
+      }
+      if (!kept) {
 #pragma unroll
-      for (int i = PER - 1; i >= 0; --i)
-        if (key[i] == top) cand = (uint32_t)(lane + 32 * i);
-      const int win = (int)__reduce_min_sync(kAll, cand);
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (lane + 32 * i == win) key[i] = 0;
-      if (lane == j) {
-        my_id = win;
-        usable = top > key64(-INFINITY);
+        for (int i = 0; i < M; ++i) a[i] = 0;
       }
     }
+    // Candidates in falling order: k of them, and on until one is clearly below the
+    // k-th.  ``count`` of them once that is settled, ``near`` if a gap between two
+    // was too narrow to tell their order.
+    const int cand = d.groups > 1 ? o.topk_group * d.size : E;
+    float last = 0.0f;
+    bool near = false;
+    int count = 0;
+#pragma unroll 1
+    for (int r = 0;; ++r) {
+      const uint32_t top = token_max<LT>(a[0]);
+      const float v = value(top);
+      const bool gap = last - v > err + REL * fabsf(last);
+      if (count == 0) {
+        if (r >= k && (gap || r == cand)) count = r;
+        else near |= r > 0 && !gap;
+      }
+      last = v;
+      if (r >= k && (r == LIST || __all_sync(kAll, count > 0))) break;
+      const uint32_t b = __ballot_sync(kAll, a[0] == top);
+      if (a[0] == top && top && !(b & mask & ((1u << lane) - 1u))) {
+        list[r] = (int16_t)expert((int)(LOW - (top & LOW)));
+#pragma unroll
+        for (int i = 0; i + 1 < M; ++i) a[i] = a[i + 1];
+        a[M - 1] = 0;
+        // more than it kept may be wanted of this lane
+        if (M < PER && a[0] == 0 && nv > M) all_again = true;
+      }
+    }
+    all_again |= count == 0;
+    // tokens whose order is open, one at a time
+    const uint32_t wide = __ballot_sync(kAll, all_again), close = __ballot_sync(kAll, near);
+    __syncwarp();
+    if (wide | close) {
+#pragma unroll 1
+      for (int q = 0; q < TW; ++q) {
+        const uint32_t lanes = LT == 32 ? kAll : ((1u << LT) - 1u) << (q * LT);
+        const int64_t tq = base + q < T ? base + q : T - 1;
+        const float top = __shfl_sync(kAll, zmax, q * LT);
+        const int n = __shfl_sync(kAll, count, q * LT);
+        if (wide & lanes)
+          exact_choice(logits + tq * E, bias, E, k, top, o, keys_s + warp * E, list_s[warp][q]);
+        else if (close & lanes)
+          rank_exactly(logits + tq * E, bias, E, top, sigmoid, n, list_s[warp][q]);
+      }
+      __syncwarp();
+    }
+    // weights in fp64
+    const bool mine = tl < k && base + tw < T;
+    const int id = mine ? list[tl] : 0;
     double s = 0.0;
-    if (lane < k && usable) s = score64(clamp_logit(__ldg(zr + my_id)), zmax, inv, sigmoid);
+    if (mine) {
+      const float b = bias ? __ldg(bias + id) : 0.0f;
+      if (b > -INFINITY)  // else (or NaN) not available, as by its logit
+        s = score64(clamp_logit(__ldg(zr + id)), zmax, o.renorm ? 1.0 : 1.0 / den, sigmoid);
+    }
     double wt = s;
     if (o.renorm) {
-      double den = s;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(kAll, den, off);
-      wt = den > 0.0 ? s / den : 0.0;
+      const double sum = token_sum<LT>(s);
+      wt = sum > 0.0 ? s / sum : 0.0;
     }
     wt *= (double)o.factor;
-    if (lane < k) {
-      if (scale) wt *= (double)__ldg(scale + my_id);
-      ids[t * k + lane] = my_id;
-      w[t * k + lane] = (float)wt;
-      if (load) atomicAdd(&hist[my_id], 1);
+    if (mine) {
+      if (scale) wt *= (double)__ldg(scale + id);
+      ids[t * k + tl] = id;
+      w[t * k + tl] = (float)wt;
+      if (load) atomicAdd(&hist[id], 1);
     }
+    __syncwarp();
   }
   if (load) {
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x)
-      if (hist[e]) atomicAdd(load + e, hist[e]);
+    // alone, a block writes the counts; several add theirs to zeros
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      if (gridDim.x == 1) load[e] = hist[e];
+      else if (hist[e]) atomicAdd(load + e, hist[e]);
+    }
   }
+}
+
+// Zeros ahead of a launch of several blocks, which starts beside it.
+__global__ void zero_load_kernel(int32_t* load, int E) {
+  pdl_trigger();
+  pdl_wait();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) load[e] = 0;
+}
+
+template <int LT, bool K8>
+cudaError_t launch_balance(int per, unsigned blocks, unsigned threads, const float* logits,
+                           const float* bias, const float* scale, int64_t T, int E, int k,
+                           int32_t* ids, float* w, int32_t* load, const BalanceOpt& o,
+                           const Deal& d, cudaStream_t st) {
+  auto kern = per <= 1    ? balance_kernel<LT, 1, K8>
+              : per <= 2  ? balance_kernel<LT, 2, K8>
+              : per <= 4  ? balance_kernel<LT, 4, K8>
+              : per <= 8  ? balance_kernel<LT, 8, K8>
+              : per <= 16 ? balance_kernel<LT, 16, K8>
+                          : balance_kernel<LT, 32, K8>;
+  const size_t smem = sizeof(unsigned long long) * (threads / 32) * E;
+  if (smem > 32 * 1024) {
+    // (the opt-in is per device; the largest E and block take 64 KB)
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, logits, bias, scale, T, E, k,
+                   ids, w, load, o, d);
+}
+
+// Deals E experts in groups to LT lanes; n > 32 where they do not fit.
+Deal deal(int E, int groups, int LT, bool aligned) {
+  Deal d{groups, E / groups, LT, 0, 0};
+  while (d.lanes * groups > LT) d.lanes /= 2;  // 0: more groups than lanes
+  if (d.lanes == 0) {
+    d.n = 1 << 20;
+    return d;
+  }
+  d.n = (d.size + d.lanes - 1) / d.lanes;
+  const int quads = (d.size + 4 * d.lanes - 1) / (4 * d.lanes);
+  if (aligned && d.size % 4 == 0 && d.n >= 4) {
+    d.quads = 1;
+    d.n = 4 * quads;
+  }
+  return d;
 }
 
 }  // namespace
@@ -220,14 +603,39 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
     }
   }
   if (shape->T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
-  if (load && cudaMemsetAsync(load, 0, sizeof(int32_t) * E, stream) != cudaSuccess)
+  const int64_t T = shape->T;
+  const bool vec = ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0;
+  // A warp per token while that leaves the SMs room; else the fewest lanes that the
+  // groups and 32 experts a lane allow.
+  int LT = 32;
+  Deal d = deal(E, o.n_group, 32, vec);
+  if (k <= 8 && T > 8 * device_sm_count()) {
+    for (int lt = 8; lt < 32; lt *= 2) {
+      const Deal c = deal(E, o.n_group, lt, vec);
+      if (c.n > 32) continue;
+      LT = lt;
+      d = c;
+      break;
+    }
+  }
+  const int tw = 32 / LT;
+  const int64_t need = (T + tw - 1) / tw;  // warps
+  const int warps = need < kRouteWarps ? (need > 0 ? (int)need : 1) : kRouteWarps;
+  const int64_t all = (need + warps - 1) / warps, most = 4 * device_sm_count();
+  const unsigned blocks = (unsigned)(all < most ? all : most);
+  if (load && blocks != 1 &&
+      launch_ex(zero_load_kernel, dim3(1), dim3(256), 0, stream, true, load, E) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (shape->T == 0) return MOE_OK;
-  auto kern = E <= 32 ? balance_kernel<1> : E <= 64 ? balance_kernel<2> : E <= 128 ? balance_kernel<4>
-              : E <= 256 ? balance_kernel<8> : balance_kernel<16>;
-  const int64_t blocks = (shape->T + 7) / 8;
+  if (T == 0) return MOE_OK;
+  const unsigned threads = 32 * warps;
   const cudaError_t e =
-      launch_ex(kern, dim3((unsigned)blocks), dim3(256), load ? sizeof(int32_t) * E : 0, stream,
-                false, logits, bias, scale, shape->T, E, k, ids, w, load, o);
+      LT == 8    ? launch_balance<8, true>(d.n, blocks, threads, logits, bias, scale, T, E, k, ids,
+                                           w, load, o, d, stream)
+      : LT == 16 ? launch_balance<16, true>(d.n, blocks, threads, logits, bias, scale, T, E, k,
+                                            ids, w, load, o, d, stream)
+      : k <= 8   ? launch_balance<32, true>(d.n, blocks, threads, logits, bias, scale, T, E, k,
+                                            ids, w, load, o, d, stream)
+                 : launch_balance<32, false>(d.n, blocks, threads, logits, bias, scale, T, E, k,
+                                             ids, w, load, o, d, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
