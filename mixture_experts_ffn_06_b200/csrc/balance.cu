@@ -276,7 +276,7 @@ __device__ __forceinline__ double token_sum(double v) {
 // group, or with quads four at a time, read as 16-byte vectors.
 struct Deal {
   int groups, size;  // 1 and E without groups
-  int lanes;         // lanes per group
+  int lanes, lg;     // lanes per group, and its logarithm
   int n;             // experts per lane, at most
   int quads;
 };
@@ -305,15 +305,16 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int tl = lane % LT, tw = lane / LT;
   const uint32_t mask = LT == 32 ? kAll : ((1u << LT) - 1u) << (tw * LT);  // this token's lanes
+  const uint32_t below = mask & ((1u << lane) - 1u);
   const bool sigmoid = o.scoring == MOE_SCORE_SIGMOID;
-  const int g = tl / d.lanes, sub = tl % d.lanes;  // this lane's group and place in it
+  const int g = tl >> d.lg, sub = tl & (d.lanes - 1);  // this lane's group and place in it
   const bool in = g < d.groups;
   // its first expert, and how many it has
   const int e0 = g * d.size + (d.quads ? 4 * sub : sub);
   int nv = 0;
   if (in)
-    nv = d.quads ? 4 * ((d.size - 4 * sub + 4 * d.lanes - 1) / (4 * d.lanes))
-                 : (d.size - sub + d.lanes - 1) / d.lanes;
+    nv = d.quads ? 4 * ((d.size - 4 * sub + 4 * d.lanes - 1) >> (d.lg + 2))
+                 : (d.size - sub + d.lanes - 1) >> d.lg;
   const int step = d.quads ? 4 * d.lanes : d.lanes;
   auto expert = [&](int i) { return d.quads ? e0 + (i >> 2) * step + (i & 3) : e0 + i * step; };
   int16_t* list = list_s[warp][tw];
@@ -329,6 +330,7 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
     const int64_t t = base + tw < T ? base + tw : T - 1;
     const float* zr = logits + t * E;
     float z[PER];
+    float early[PER <= 8 ? PER : 1];  // the bias, requested beside the logits
     float zmax = -INFINITY;
     bool quads = false;
     if constexpr (PER >= 4) {
@@ -348,6 +350,11 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
     if (!quads) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) z[i] = i < nv ? __ldg(zr + e0 + i * step) : -INFINITY;
+    }
+    if constexpr (PER <= 8) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        early[i] = bias && i < nv ? __ldg(bias + expert(i)) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -390,8 +397,10 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
       const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
       a[i] = i < nv ? (key & ~LOW) | (LOW - i) : 0u;
     };
-    if constexpr (PER >= 4) {
-      if (quads) {
+    if constexpr (PER <= 8) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) pack(i, early[i]);
+    } else if (quads) {
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
           float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -402,9 +411,7 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
           pack(i + 2, b.z);
           pack(i + 3, b.w);
         }
-      }
-    }
-    if (!quads) {
+    } else {
 #pragma unroll
       for (int i = 0; i < PER; ++i) pack(i, bias && i < nv ? __ldg(bias + e0 + i * step) : 0.f);
     }
@@ -430,7 +437,7 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
       int rank = 0;
       for (int s = d.lanes; s < LT; s += d.lanes) {
         const float other = __shfl_xor_sync(kAll, score, s);
-        const int og = (tl ^ s) / d.lanes;
+        const int og = (tl ^ s) >> d.lg;
         rank += og < d.groups && (other > score || (other == score && og < g));
       }
       const bool kept = in && rank < o.topk_group;
@@ -447,25 +454,12 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
       }
     }
     // Candidates in falling order: k of them, and on until one is clearly below the
-    // k-th.  ``count`` of them once that is settled, ``near`` if a gap between two
-    // was too narrow to tell their order.
+    // k-th: ``count`` of them then.  ``near``: a gap between two was too narrow to
+    // tell their order.
     const int cand = d.groups > 1 ? o.topk_group * d.size : E;
-    float last = 0.0f;
-    bool near = false;
-    int count = 0;
-#pragma unroll 1
-    for (int r = 0;; ++r) {
-      const uint32_t top = token_max<LT>(a[0]);
-      const float v = value(top);
-      const bool gap = last - v > err + REL * fabsf(last);
-      if (count == 0) {
-        if (r >= k && (gap || r == cand)) count = r;
-        else near |= r > 0 && !gap;
-      }
-      last = v;
-      if (r >= k && (r == LIST || __all_sync(kAll, count > 0))) break;
+    auto pop = [&](int r, uint32_t top) {
       const uint32_t b = __ballot_sync(kAll, a[0] == top);
-      if (a[0] == top && top && !(b & mask & ((1u << lane) - 1u))) {
+      if (a[0] == top && !(b & below) && top) {
         list[r] = (int16_t)expert((int)(LOW - (top & LOW)));
 #pragma unroll
         for (int i = 0; i + 1 < M; ++i) a[i] = a[i + 1];
@@ -473,6 +467,28 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
         // more than it kept may be wanted of this lane
         if (M < PER && a[0] == 0 && nv > M) all_again = true;
       }
+    };
+    uint32_t top = token_max<LT>(a[0]);
+    float v = value(top), last = v;
+    bool near = false;
+#pragma unroll 1
+    for (int r = 0; r < k; ++r) {
+      pop(r, top);
+      top = token_max<LT>(a[0]);
+      const float tol = err + REL * fabsf(v), before = v;
+      v = value(top);
+      if (r + 1 < k) near |= !(before - v > tol);
+      else last = before;
+    }
+    int count = last - v > err + REL * fabsf(last) || k == cand ? k : 0;
+#pragma unroll 1
+    for (int r = k; r < LIST && __any_sync(kAll, count == 0); ++r) {
+      near |= count == 0;
+      pop(r, top);
+      last = v;
+      top = token_max<LT>(a[0]);
+      v = value(top);
+      if (count == 0 && (last - v > err + REL * fabsf(last) || r + 1 == cand)) count = r + 1;
     }
     all_again |= count == 0;
     // tokens whose order is open, one at a time
@@ -495,6 +511,7 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
     // weights in fp64
     const bool mine = tl < k && base + tw < T;
     const int id = mine ? list[tl] : 0;
+    const float each = scale && mine ? __ldg(scale + id) : 1.0f;
     double s = 0.0;
     if (mine) {
       const float b = bias ? __ldg(bias + id) : 0.0f;
@@ -508,9 +525,8 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
     }
     wt *= (double)o.factor;
     if (mine) {
-      if (scale) wt *= (double)__ldg(scale + id);
       ids[t * k + tl] = id;
-      w[t * k + tl] = (float)wt;
+      w[t * k + tl] = (float)(wt * (double)each);
       if (load) atomicAdd(&hist[id], 1);
     }
     __syncwarp();
@@ -556,12 +572,13 @@ cudaError_t launch_balance(int per, unsigned blocks, unsigned threads, const flo
 
 // Deals E experts in groups to LT lanes; n > 32 where they do not fit.
 Deal deal(int E, int groups, int LT, bool aligned) {
-  Deal d{groups, E / groups, LT, 0, 0};
+  Deal d{groups, E / groups, LT, 0, 0, 0};
   while (d.lanes * groups > LT) d.lanes /= 2;  // 0: more groups than lanes
   if (d.lanes == 0) {
     d.n = 1 << 20;
     return d;
   }
+  while (1 << d.lg < d.lanes) ++d.lg;
   d.n = (d.size + d.lanes - 1) / d.lanes;
   const int quads = (d.size + 4 * d.lanes - 1) / (4 * d.lanes);
   if (aligned && d.size % 4 == 0 && d.n >= 4) {
