@@ -76,24 +76,42 @@ __device__ __forceinline__ double softmax_inverse64(const float* __restrict__ zr
   return 1.0 / sum;
 }
 
-// Puts n <= 32 candidates of a token in the order of their fp64 values (equal ones
-// by id), by the whole warp: each lane forms one and counts those before it.
+// c of an expert as the choice compares it, in fp32: ``term`` is the logit, or the
+// softmax's exponential.
+__device__ __forceinline__ float choice32(float term, float inv, float b, bool sigmoid) {
+  const float c = (sigmoid ? __fdividef(1.0f, 1.0f + __expf(-term)) : term * inv) + b;
+  return available(term) && c == c ? c : -INFINITY;
+}
+
+// Puts n <= 32 candidates of a token in their order, by the whole warp: each lane
+// forms one's value and counts those before it.  In fp32 first, without the
+// packing's error; where two are still within err of each other, in fp64, equal
+// values by id.
 __device__ __noinline__ void rank_exactly(const float* __restrict__ zr,
                                           const float* __restrict__ bias, int E, float zmax,
-                                          bool sigmoid, int n, int16_t* list) {
+                                          float inv, float err, bool sigmoid, int n,
+                                          int16_t* list) {
   const int lane = threadIdx.x & 31;
-  const double inv = sigmoid ? 1.0 : softmax_inverse64(zr, E, zmax);
   const int id = lane < n ? list[lane] : E;
-  double c = -INFINITY;
-  if (lane < n) {
-    const float z = clamp_logit(__ldg(zr + id));
-    c = choice64(z, score64(z, zmax, inv, sigmoid), bias ? __ldg(bias + id) : 0.f);
-  }
+  const float z = lane < n ? clamp_logit(__ldg(zr + id)) : 0.f;
+  const float b = lane < n && bias ? __ldg(bias + id) : 0.f;
+  const float c = choice32(sigmoid || !available(z) ? z : __expf(z - zmax), inv, b, sigmoid);
   int rank = 0;
+  bool close = false;
   for (int i = 0; i < n; ++i) {
-    const double ci = __shfl_sync(kAll, c, i);
-    const int idi = __shfl_sync(kAll, id, i);
-    rank += ci > c || (ci == c && idi < id);
+    const float ci = __shfl_sync(kAll, c, i);
+    rank += ci > c;
+    close |= i != lane && !(fabsf(ci - c) > err + 4.8e-07f * fabsf(c));
+  }
+  if (__any_sync(kAll, close && lane < n)) {
+    const double all = sigmoid ? 1.0 : softmax_inverse64(zr, E, zmax);
+    const double d = choice64(z, score64(z, zmax, all, sigmoid), b);
+    rank = 0;
+    for (int i = 0; i < n; ++i) {
+      const double di = __shfl_sync(kAll, d, i);
+      const int idi = __shfl_sync(kAll, id, i);
+      rank += di > d || (di == d && idi < id);
+    }
   }
   __syncwarp();  // every lane has read its entry
   if (lane < n) list[rank] = (int16_t)id;
@@ -281,16 +299,10 @@ struct Deal {
   int quads;
 };
 
-constexpr int kRouteWarps = 16;
-
-// c of an expert as the choice compares it, in fp32.
-__device__ __forceinline__ float choice32(float term, float inv, float b, bool sigmoid) {
-  const float c = (sigmoid ? __fdividef(1.0f, 1.0f + __expf(-term)) : term * inv) + b;
-  return available(term) && c == c ? c : -INFINITY;
-}
+constexpr int kRouteWarps = 8;
 
 template <int LT, int PER, bool K8>  // K8: k <= 8
-__global__ void __launch_bounds__(32 * kRouteWarps, PER <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kRouteWarps, PER <= 8 ? 4 : PER <= 16 ? 3 : 2)
 balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
                const float* __restrict__ scale, int64_t T, int E, int k,
                int32_t* __restrict__ ids, float* __restrict__ w, int32_t* __restrict__ load,
@@ -501,10 +513,11 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
         const int64_t tq = base + q < T ? base + q : T - 1;
         const float top = __shfl_sync(kAll, zmax, q * LT);
         const int n = __shfl_sync(kAll, count, q * LT);
+        const float invq = __shfl_sync(kAll, inv, q * LT), errq = __shfl_sync(kAll, err, q * LT);
         if (wide & lanes)
           exact_choice(logits + tq * E, bias, E, k, top, o, keys_s + warp * E, list_s[warp][q]);
         else if (close & lanes)
-          rank_exactly(logits + tq * E, bias, E, top, sigmoid, n, list_s[warp][q]);
+          rank_exactly(logits + tq * E, bias, E, top, invq, errq, sigmoid, n, list_s[warp][q]);
       }
       __syncwarp();
     }
@@ -559,13 +572,7 @@ cudaError_t launch_balance(int per, unsigned blocks, unsigned threads, const flo
               : per <= 8  ? balance_kernel<LT, 8, K8>
               : per <= 16 ? balance_kernel<LT, 16, K8>
                           : balance_kernel<LT, 32, K8>;
-  const size_t smem = sizeof(unsigned long long) * (threads / 32) * E;
-  if (smem > 32 * 1024) {
-    // (the opt-in is per device; the largest E and block take 64 KB)
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-    if (e != cudaSuccess) return e;
-  }
+  const size_t smem = sizeof(unsigned long long) * (threads / 32) * E;  // at most 32 KB
   return launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, logits, bias, scale, T, E, k,
                    ids, w, load, o, d);
 }
@@ -638,7 +645,7 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
   const int tw = 32 / LT;
   const int64_t need = (T + tw - 1) / tw;  // warps
   const int warps = need < kRouteWarps ? (need > 0 ? (int)need : 1) : kRouteWarps;
-  const int64_t all = (need + warps - 1) / warps, most = 4 * device_sm_count();
+  const int64_t all = (need + warps - 1) / warps, most = 8 * device_sm_count();
   const unsigned blocks = (unsigned)(all < most ? all : most);
   if (load && blocks != 1 &&
       launch_ex(zero_load_kernel, dim3(1), dim3(256), 0, stream, true, load, E) != cudaSuccess)
