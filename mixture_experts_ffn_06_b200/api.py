@@ -427,26 +427,33 @@ def moe_forward_fp8(shape, x, logits, weights: moe_fp8_experts, scale, out, ws,
 # ------------------------------------------------ next to the expert products
 #
 # These calls are made once or twice per block and token step, so their own
-# cost counts at small T: the checks read tensor attributes only.  Unlike a raw
-# pointer, a tensor of the wrong type, size or device is refused here.
+# cost counts at small T: the checks read tensor attributes only, and the device
+# is asked for once.  Unlike a raw pointer, a tensor of the wrong type, size or
+# device is refused here.
 
-def _q(t, dtype, numel, what):
-    """The address of a contiguous CUDA tensor of ``numel`` ``dtype`` values on
-    the current device, None for None."""
+_cuda_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+_cuda_stream = torch._C._cuda_getCurrentRawStream \
+    if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda dev: torch.cuda.current_stream(dev).cuda_stream
+
+
+def _q(t, dtype, numel, dev, what):
+    """The address of a contiguous tensor of ``numel`` ``dtype`` values on CUDA
+    device ``dev``, None for None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.numel() == numel and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of {numel} values, "
                          f"got {tuple(t.shape)} {t.dtype}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what}: expected a tensor on the current CUDA device")
-    return t.data_ptr()
+    raise ValueError(f"{what}: expected a tensor on the current CUDA device, got {t.device}")
 
 
-def _s(stream):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+def _dev(t):
+    """The current CUDA device; a tensor elsewhere is refused by _q."""
+    return _cuda_device() if t.is_cuda else 0
 
 
 def balance_opts(scoring=SCORE_SOFTMAX, n_group=1, topk_group=1, group_top=1, renorm=True,
@@ -461,20 +468,27 @@ def moe_route_balanced(shape, logits, bias, scale, ids, w, load=None, opts=None,
     int32 and w [T,k] fp32 out, ``load`` [E] int32 out or None (choices per
     expert, overwritten); ``opts`` from balance_opts()."""
     T, E, k = shape.T, shape.E, shape.k
-    f32, i32 = torch.float32, torch.int32
-    _check(lib.moe_route_balanced(
-        shape, _q(logits, f32, T * E, "logits"), _q(bias, f32, E, "bias"),
-        _q(scale, f32, E, "scale"), opts, _q(ids, i32, T * k, "ids"), _q(w, f32, T * k, "w"),
-        _q(load, i32, E, "load"), _s(stream)), "moe_route_balanced")
+    f32, i32, d = torch.float32, torch.int32, _dev(logits)
+    st = lib.moe_route_balanced(
+        shape, _q(logits, f32, T * E, d, "logits"), _q(bias, f32, E, d, "bias"),
+        _q(scale, f32, E, d, "scale"), opts, _q(ids, i32, T * k, d, "ids"),
+        _q(w, f32, T * k, d, "w"), _q(load, i32, E, d, "load"),
+        _cuda_stream(d) if stream is None else stream.cuda_stream)
+    if st:
+        raise MoEError(st, "moe_route_balanced")
 
 
 def moe_quantize_rows_i8(src, codes, scales, stream=None):
     """Per-row dynamic int8 quantisation of bf16 rows src [R, C] into codes
     (int8 [R, C]) and scales (fp32 [R])."""
     R, C = src.shape
-    _check(lib.moe_quantize_rows_i8(
-        _q(src, torch.bfloat16, R * C, "src"), R, C, _q(codes, torch.int8, R * C, "codes"),
-        _q(scales, torch.float32, R, "scales"), _s(stream)), "moe_quantize_rows_i8")
+    d = _dev(src)
+    st = lib.moe_quantize_rows_i8(
+        _q(src, torch.bfloat16, R * C, d, "src"), R, C, _q(codes, torch.int8, R * C, d, "codes"),
+        _q(scales, torch.float32, R, d, "scales"),
+        _cuda_stream(d) if stream is None else stream.cuda_stream)
+    if st:
+        raise MoEError(st, "moe_quantize_rows_i8")
 
 
 def moe_linear_i8(x, x_scale, w, w_scale, out, ws, gate_act=None, out_f32=None, stream=None):
@@ -485,13 +499,17 @@ def moe_linear_i8(x, x_scale, w, w_scale, out, ws, gate_act=None, out_f32=None, 
     (uint8), zeroed once; its error word is read by moe_read_error."""
     T, K = x.shape
     N = w.shape[0]
-    n_out = T * (N if gate_act is None else N // 2)
-    i8, f32 = torch.int8, torch.float32
-    _check(lib.moe_linear_i8(
-        T, N, K, _q(x, i8, T * K, "x"), _q(x_scale, f32, T, "x_scale"), _q(w, i8, N * K, "w"),
-        _q(w_scale, f32, N, "w_scale"), LINEAR_PLAIN if gate_act is None else gate_act,
-        _q(out, torch.bfloat16, n_out, "out"), _q(out_f32, f32, n_out, "out_f32"),
-        _q(ws, torch.uint8, ws.numel(), "ws"), ws.numel(), _s(stream)), "moe_linear_i8")
+    d, i8, f32 = _dev(x), torch.int8, torch.float32
+    n_out, n_ws = T * (N if gate_act is None else N // 2), ws.numel()
+    st = lib.moe_linear_i8(
+        T, N, K, _q(x, i8, T * K, d, "x"), _q(x_scale, f32, T, d, "x_scale"),
+        _q(w, i8, N * K, d, "w"), _q(w_scale, f32, N, d, "w_scale"),
+        LINEAR_PLAIN if gate_act is None else gate_act,
+        _q(out, torch.bfloat16, n_out, d, "out"), _q(out_f32, f32, n_out, d, "out_f32"),
+        _q(ws, torch.uint8, n_ws, d, "ws"), n_ws,
+        _cuda_stream(d) if stream is None else stream.cuda_stream)
+    if st:
+        raise MoEError(st, "moe_linear_i8")
 
 
 def moe_block_norm(r, y=None, post_w=None, gate=None, token_gate=None, alpha=1.0, beta=1.0,
@@ -503,10 +521,13 @@ def moe_block_norm(r, y=None, post_w=None, gate=None, token_gate=None, alpha=1.0
     [T,H] and scales [T].  post_w, pre_w and gate [H] bf16, token_gate [T]
     fp32.  r_out may be r."""
     T, H = r.shape
-    n, bf, f32 = T * H, torch.bfloat16, torch.float32
+    n, d, bf, f32 = T * H, _dev(r), torch.bfloat16, torch.float32
     prm = moe_block_norm_params(
-        _q(y, bf, n, "y"), _q(r, bf, n, "r"), _q(post_w, bf, H, "post_w"),
-        _q(gate, bf, H, "gate"), _q(token_gate, f32, T, "token_gate"),
-        _q(pre_w, bf, H, "pre_w"), alpha, beta, post_eps, pre_eps, _q(r_out, bf, n, "r_out"),
-        _q(a, bf, n, "a"), _q(codes, torch.int8, n, "codes"), _q(scales, f32, T, "scales"))
-    _check(lib.moe_block_norm(T, H, prm, _s(stream)), "moe_block_norm")
+        _q(y, bf, n, d, "y"), _q(r, bf, n, d, "r"), _q(post_w, bf, H, d, "post_w"),
+        _q(gate, bf, H, d, "gate"), _q(token_gate, f32, T, d, "token_gate"),
+        _q(pre_w, bf, H, d, "pre_w"), alpha, beta, post_eps, pre_eps,
+        _q(r_out, bf, n, d, "r_out"), _q(a, bf, n, d, "a"),
+        _q(codes, torch.int8, n, d, "codes"), _q(scales, f32, T, d, "scales"))
+    st = lib.moe_block_norm(T, H, prm, _cuda_stream(d) if stream is None else stream.cuda_stream)
+    if st:
+        raise MoEError(st, "moe_block_norm")
