@@ -771,9 +771,10 @@ LinPlan plan_tiles(int64_t T, int mt128, int KB, int sms) {
     const int tt0 = ceil_div(T, 256 * nsub);
     for (int tt = tt0; tt <= tt0 + 4; ++tt) {
       const int per = ceil_div(T, (int64_t)tt * nsub);
-      // CTA pairs halve what each SM loads of the tokens: worth it for long sums
-      // over several rounds (K = 4096, T = 4096: 355 against 368 us; K = 2816,
-      // T = 8192: 91 against 86 us) and for 512 columns (T = 512: 31 against 36 us)
+      // CTA pairs halve what each SM loads of the tokens: worth their start-up over
+      // several rounds (loops of the same call, under the power limit: K = 4096, T =
+      // 4096 401 against 415 us; K = 2816, T = 8192 95 against 98; one round, K =
+      // 2816, T = 512: 14.3 against 13.1) and for 512 columns (T = 512: 31 against 36)
       int cg = 1;
       int64_t rounds = 0;
       int tn = 0, TT = 0;
@@ -781,7 +782,7 @@ LinPlan plan_tiles(int64_t T, int mt128, int KB, int sms) {
         tn = 16 * cg * ceil_div(per, 16 * cg);
         TT = ceil_div(T, (int64_t)tn * nsub);
         rounds = (ceil_div(mt128, cg) * (int64_t)TT + sms / cg - 1) / (sms / cg);
-        if (cg == 1 && ((KB >= 32 && rounds >= 4) || nsub * tn > 384)) cg = 2;
+        if (cg == 1 && (rounds >= 4 || nsub * tn > 384)) cg = 2;
         else break;
       }
       if (tn > 256) continue;

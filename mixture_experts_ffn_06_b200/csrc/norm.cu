@@ -263,7 +263,7 @@ cudaError_t launch_rows(int64_t rows, RowParams& p, cudaStream_t st) {
   if (rows > 2 * device_sm_count()) {
     nt = (p.vec + 127) / 128 * 32;
     const int nt3 = (p.vec + 95) / 96 * 32;
-    if (3 * nt3 <= 4 * nt) nt = nt3;
+    if (nt3 <= 1024 && 3 * nt3 <= 4 * nt) nt = nt3;
     if (p.vec <= 128) nt = 32, per = 8;
   }
   const int vpt = (p.vec + nt - 1) / nt;

@@ -81,17 +81,60 @@ def test_matches_the_definition(api, case, with_bias):
     _check(_run(api, z, k, bias, scale, **opts), ref.route(z, k, bias, scale, **opts))
 
 
+# many tokens: 8 or 16 lanes to a token, experts read in quads or one by one
+MANY = [
+    (1301, 8, 2, 0, 1, 1, 1, True, 1.0),
+    (1301, 64, 6, 0, 1, 1, 1, False, 1.0),
+    (1303, 66, 8, 1, 1, 1, 1, True, 1.0),
+    (1200, 128, 8, 1, 1, 1, 1, True, 1.0),
+    (1300, 256, 8, 1, 8, 4, 2, True, 2.5),
+    (1300, 250, 8, 0, 1, 1, 1, True, 1.0),
+    (1300, 256, 8, 0, 4, 3, 1, False, 1.0),
+    (1300, 512, 8, 1, 1, 1, 1, True, 1.0),
+    (1300, 500, 7, 1, 5, 2, 2, True, 1.0),
+    (1300, 96, 8, 1, 3, 1, 2, True, 1.0),
+    (1300, 160, 6, 0, 16, 5, 2, True, 1.0),
+    (1300, 510, 8, 1, 17, 9, 2, True, 1.0),
+    (1300, 128, 12, 0, 1, 1, 1, True, 1.0),
+    (20000, 32, 4, 1, 1, 1, 1, True, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "T%d-E%d-k%d-s%d-g%d" % c[:5])
+def test_many_tokens(api, case):
+    test_matches_the_definition(api, case, True)
+
+
+@pytest.mark.parametrize("T", [40, 1300])
+@pytest.mark.parametrize("scoring", [0, 1])
+@pytest.mark.parametrize("spread", [0.0, 1e-7, 1e-3])
+def test_the_largest_together(api, T, scoring, spread):
+    # the largest logits on the experts that one lane holds, apart by nothing, by less
+    # than fp32 tells and by more; and more near equals than a candidate list takes
+    g = np.random.default_rng(11)
+    E, k = 256, 8
+    z = g.standard_normal((T, E)).astype(np.float32)
+    one_lane = [q * 32 + i for q in range(8) for i in range(4)]
+    for t in range(T):
+        at = one_lane[:9 + t % 20] if t % 2 else g.permutation(E)[:6 + t % 30]
+        z[t, at] = (4.0 + spread * g.standard_normal(len(at))).astype(np.float32)
+    for n_group in (1, 8):
+        opts = dict(scoring=scoring, n_group=n_group, topk_group=4 if n_group > 1 else 1, group_top=2)
+        _check(_run(api, z, k, **opts), ref.route(z, k, **opts))
+
+
 def test_defaults_without_options_and_load(api):
     z = np.random.default_rng(0).standard_normal((50, 24)).astype(np.float32)
     _check(_run(api, z, 3, with_load=False), ref.route(z, 3))
 
 
+@pytest.mark.parametrize("T", [300, 1300])
 @pytest.mark.parametrize("scoring", [0, 1])
-def test_close_choices_are_ranked_as_real_numbers(api, scoring):
+def test_close_choices_are_ranked_as_real_numbers(api, scoring, T):
     # scores that fp32 cannot tell apart: logits one ulp apart, with biases that
     # bring far scores together to within 1e-9
     g = np.random.default_rng(5)
-    T, E, k = 300, 64, 8
+    E, k = 64, 8
     z = np.full((T, E), 0.5, np.float32)
     steps = g.permuted(np.tile(np.arange(E), (T, 1)), axis=1)
     z = (z.view(np.uint32) + steps.astype(np.uint32)).view(np.float32)
@@ -108,9 +151,10 @@ def test_close_choices_are_ranked_as_real_numbers(api, scoring):
 
 @pytest.mark.parametrize("n_group,topk_group,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
 @pytest.mark.parametrize("scoring", [0, 1])
-def test_equal_values_go_to_the_lower_id(api, scoring, n_group, topk_group, group_top):
+@pytest.mark.parametrize("T", [200, 1300])
+def test_equal_values_go_to_the_lower_id(api, T, scoring, n_group, topk_group, group_top):
     g = np.random.default_rng(6)
-    z = g.integers(-1, 2, (200, 48)).astype(np.float32)  # many equal logits
+    z = g.integers(-1, 2, (T, 48)).astype(np.float32)  # many equal logits
     z[0] = 0.0
     z[1] = -0.0
     z[2] = 60.0   # sigmoid is 1 in fp64
@@ -121,10 +165,11 @@ def test_equal_values_go_to_the_lower_id(api, scoring, n_group, topk_group, grou
 @pytest.mark.parametrize("n_group,topk_group,group_top", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
 @pytest.mark.parametrize("scoring", [0, 1])
 @pytest.mark.parametrize("renorm", [True, False])
-def test_masked_and_special_logits(api, scoring, renorm, n_group, topk_group, group_top):
+@pytest.mark.parametrize("T", [40, 1300])
+def test_masked_and_special_logits(api, T, scoring, renorm, n_group, topk_group, group_top):
     g = np.random.default_rng(7)
     E, k = 64, 6
-    z = g.standard_normal((40, E)).astype(np.float32)
+    z = g.standard_normal((T, E)).astype(np.float32)
     z[0] = -np.inf                       # nothing available
     z[1] = np.nan
     z[2, :E - 3] = -np.inf               # fewer available than k

@@ -77,7 +77,8 @@ def _check(d, got, **kw):
 
 
 SIZES = [(1, 8), (1, 2816), (3, 256), (37, 200), (64, 2048), (130, 2816), (5, 4096), (7, 8192),
-         (2, 14336), (3, 32768), (1025, 1032), (2000, 264)]
+         (2, 14336), (3, 32768), (1025, 1032), (2000, 264), (300, 32000), (310, 32768), (500, 5632),
+         (301, 1024), (999, 8)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)

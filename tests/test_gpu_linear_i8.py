@@ -82,6 +82,37 @@ def test_gated_product(api, T, N, K, act):
     _check(_run(api, x, xs, w, ws, act), ref.linear_i8(x, xs, w, ws, act), act)
 
 
+# sizes that reach the forms the small ones do not: many small blocks, unsplit K
+# at few tokens, several tiles to a CTA and to a CTA pair, two token sub-tiles to a
+# weight tile on single CTAs and on pairs
+FORMS = [(8, 14336, 64), (3, 20000, 48), (12, 9000, 128), (40, 20000, 128), (700, 14000, 640),
+         (600, 14336, 256), (2000, 16384, 256), (257, 14336, 2064), (512, 18944, 2704),
+         (1024, 18944, 4112), (1030, 18944, 2704), (5000, 640, 1040)]
+
+
+@pytest.mark.parametrize("T,N,K", FORMS)
+@pytest.mark.parametrize("act", [None, 0])
+def test_every_form(api, T, N, K, act):
+    g = torch.Generator(device="cuda").manual_seed(T + N + K)
+    x, w = (torch.randint(-128, 128, (n, K), dtype=torch.int8, device="cuda", generator=g) for n in (T, N))
+    xs = (0.5 + torch.rand(T, device="cuda", generator=g)) / 127
+    ws = (0.5 + torch.rand(N, device="cuda", generator=g)) / 127 / K ** 0.5
+    n = N if act is None else N // 2
+    out = torch.full((T, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    o32 = torch.full((T, n), float("nan"), device="cuda")
+    work = _ws()
+    api.moe_linear_i8(x, xs, w, ws, out, work, gate_act=act, out_f32=o32)
+    assert api.moe_read_error(work) == 0
+    v = (x.double() @ w.double().T).float() * (xs[:, None] * ws)   # the sums are exact
+    if act is None:
+        assert torch.equal(o32, v)
+    else:
+        want = v[:, :n].double()
+        want = want / (1 + torch.exp(-want)) * v[:, n:].double()
+        assert bool(((o32 - want).abs() <= GATED_RTOL * want.abs() + GATED_ATOL).all())
+    assert torch.equal(out, o32.to(torch.bfloat16))
+
+
 @pytest.mark.parametrize("T", [1, 5, 40, 200])
 def test_extreme_codes_at_the_longest_k(api, T):
     # every product is 128 * 128: the largest sum that 32 bits hold
