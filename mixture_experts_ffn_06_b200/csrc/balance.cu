@@ -69,6 +69,7 @@ __device__ __forceinline__ double choice64(float z, double s, float b) {
 __device__ __forceinline__ double softmax_inverse64(const float* __restrict__ zr, int E,
                                                     float zmax) {
   double sum = 0.0;
+#pragma unroll 4
   for (int e = threadIdx.x & 31; e < E; e += 32)
     sum += score64(clamp_logit(__ldg(zr + e)), zmax, 1.0, false);
 #pragma unroll
@@ -117,67 +118,77 @@ __device__ __noinline__ void rank_exactly(const float* __restrict__ zr,
   if (lane < n) list[rank] = (int16_t)id;
 }
 
-// The k chosen experts of one token on fp64 values alone, by the whole warp: rounds
-// of a maximum over key[E], ordered keys in shared memory (0: not a candidate),
-// equal values to the lower id.
-__device__ __noinline__ void exact_choice(const float* __restrict__ zr,
-                                          const float* __restrict__ bias, int E, int k,
-                                          float zmax, const BalanceOpt& o,
-                                          unsigned long long* key, int16_t* out) {
+// One token's choice values in fp64 as ordered keys in key[E] (shared memory), and the
+// groups it keeps by them (a bit each), by the whole warp.
+__device__ __noinline__ uint32_t exact_groups(const float* __restrict__ zr,
+                                              const float* __restrict__ bias, int E, float zmax,
+                                              const BalanceOpt& o, unsigned long long* key) {
   const int lane = threadIdx.x & 31;
   const bool sigmoid = o.scoring == MOE_SCORE_SIGMOID;
   const double inv = sigmoid ? 1.0 : softmax_inverse64(zr, E, zmax);
+#pragma unroll 4
   for (int e = lane; e < E; e += 32) {
     const float z = clamp_logit(__ldg(zr + e));
     key[e] = key64(choice64(z, score64(z, zmax, inv, sigmoid), bias ? __ldg(bias + e) : 0.f));
   }
   __syncwarp();
-  // the largest key of [e0, e1) and the lowest id that has it; takes it out
-  auto take = [&](int e0, int e1, int* win) {
+  if (o.n_group <= 1) return kAll;
+  // a power of two lanes to a group, each with every such expert of it
+  int lanes = 32;
+  while (lanes * o.n_group > 32) lanes >>= 1;
+  const int gs = E / o.n_group, g = lane / lanes;
+  unsigned long long k0 = 0, k1 = 0;  // the two largest
+  if (g < o.n_group) {
+#pragma unroll 4
+    for (int e = lane % lanes; e < gs; e += lanes) {
+      const unsigned long long v = key[g * gs + e];
+      k1 = max(k1, min(k0, v));
+      k0 = max(k0, v);
+    }
+  }
+  for (int s = 1; s < lanes; s <<= 1) {
+    const unsigned long long w0 = __shfl_xor_sync(kAll, k0, s), w1 = __shfl_xor_sync(kAll, k1, s);
+    k1 = max(min(k0, w0), max(k1, w1));
+    k0 = max(k0, w0);
+  }
+  const double score =
+      g < o.n_group ? (o.group_top == 2 && gs > 1 ? value64(k0) + value64(k1) : value64(k0)) : 0.0;
+  int rank = 0;
+  for (int i = 0; i < o.n_group; ++i) {
+    const double other = __shfl_sync(kAll, score, i * lanes);
+    rank += other > score || (other == score && i < g);
+  }
+  const uint32_t b = __ballot_sync(kAll, g < o.n_group && rank < o.topk_group);
+  uint32_t keep = 0;
+  for (int i = 0; i < o.n_group; ++i) keep |= ((b >> (i * lanes)) & 1u) << i;
+  return keep;
+}
+
+// The k chosen experts of one token on fp64 values alone, by the whole warp: rounds
+// of a maximum over the keys, equal values to the lower id.
+__device__ __noinline__ void exact_choice(const float* __restrict__ zr,
+                                          const float* __restrict__ bias, int E, int k,
+                                          float zmax, const BalanceOpt& o,
+                                          unsigned long long* key, int16_t* out) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t keep = exact_groups(zr, bias, E, zmax, o, key);
+  if (o.n_group > 1) {
+    const int gs = E / o.n_group;
+    for (int e = lane; e < E; e += 32)
+      if (!((keep >> (e / gs)) & 1u)) key[e] = 0;  // not a candidate
+    __syncwarp();
+  }
+  for (int j = 0; j < k; ++j) {
     unsigned long long best = 0;
     uint32_t at = kAll;
-    for (int e = e0 + lane; e < e1; e += 32)
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32)
       if (key[e] > best) {
         best = key[e];
         at = (uint32_t)e;
       }
     const unsigned long long top = warp_max64(best);
-    *win = (int)__reduce_min_sync(kAll, best == top ? at : kAll);
-    return top;
-  };
-  if (o.n_group > 1) {
-    const int gs = E / o.n_group;
-    unsigned long long mine = 0;  // lane g: group g's score
-    for (int g = 0; g < o.n_group; ++g) {
-      int win;
-      const unsigned long long top = take(g * gs, g * gs + gs, &win);
-      double sum = value64(top);
-      if (o.group_top == 2 && gs > 1) {
-        __syncwarp();
-        if (lane == 0) key[win] = 0;
-        __syncwarp();
-        int unused;
-        sum += value64(take(g * gs, g * gs + gs, &unused));
-        __syncwarp();
-        if (lane == 0) key[win] = top;
-        __syncwarp();
-      }
-      if (lane == g) mine = key64(sum);
-    }
-    uint32_t keep = 0;
-    for (int r = 0; r < o.topk_group; ++r) {
-      const unsigned long long top = warp_max64(mine);
-      const int win = __ffs(__ballot_sync(kAll, mine == top)) - 1;
-      keep |= 1u << win;
-      if (lane == win) mine = 0;
-    }
-    for (int e = lane; e < E; e += 32)
-      if (!((keep >> (e / gs)) & 1u)) key[e] = 0;
-    __syncwarp();
-  }
-  for (int j = 0; j < k; ++j) {
-    int win;
-    take(0, E, &win);
+    const int win = (int)__reduce_min_sync(kAll, best == top ? at : kAll);
     __syncwarp();
     if (lane == 0) {
       key[win] = 0;
@@ -374,11 +385,12 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
       zmax = fmaxf(zmax, z[i]);  // a NaN is passed over
     }
     zmax = token_max<LT>(zmax);
-    // Scores.  The fp32 exponential is within |x| 2^-23 + 2^-22 of its value; with
-    // |x| e^-|x| < 0.37 a sigmoid is within 2^-21, and a softmax's term within
-    // 2^-21 of the largest.  Its denominator adds at most ln(512) 2^-23 + 2^-22 and
+    // Scores.  The fp32 exponential is within |x| 2^-23 + 2^-22 of its value and the
+    // division within 2^-22; s (1 - s) <= 1/4 and |x| s (1 - s) < 0.23 leave a sigmoid
+    // within 3.4e-7, and with |x| e^-|x| < 0.37 a softmax's term is within 2^-21 of
+    // the largest.  Its denominator adds at most ln(512) 2^-23 + 2^-22 and
     // 21 roundings: 2^-18 of the largest score in all.
-    float err = 9.5367432e-07f;  // 2^-20: two values
+    float err = 6.8e-07f;  // of two values
     float inv = 1.0f;
     double den = 0.0;
     if (!sigmoid) {
@@ -437,7 +449,6 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
     };
     // a packed value is short of c by less than 2^-23 PER |c|; c itself rounds once
     constexpr float REL = 2.0f * (PER + 1) * 1.1920929e-07f;
-    bool all_again = false;  // the whole choice has to be made on fp64 values
     if (d.groups > 1) {
       const bool two = o.group_top == 2 && d.size > 1;
       for (int s = 1; s < d.lanes; s <<= 1) {
@@ -452,13 +463,24 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
         const int og = (tl ^ s) >> d.lg;
         rank += og < d.groups && (other > score || (other == score && og < g));
       }
-      const bool kept = in && rank < o.topk_group;
+      bool kept = in && rank < o.topk_group;
       if (o.topk_group < d.groups) {
         // the lowest kept score against the highest other
         const float low = -token_max<LT>(kept ? -score : -INFINITY);
         const float high = token_max<LT>(in && !kept ? score : -INFINITY);
         const float mag = token_max<LT>(in ? fabsf(v0) + (two ? fabsf(v1) : 0.0f) : 0.0f);
-        all_again = !(low - high > 2.0f * err + 4.8e-07f * mag);
+        uint32_t open = __ballot_sync(kAll, !(low - high > 2.0f * err + 4.8e-07f * mag));
+#pragma unroll 1
+        while (open) {  // a token whose groups are open
+          const int q = (__ffs(open) - 1) / LT;
+          open &= LT == 32 ? 0u : ~(((1u << LT) - 1u) << (q * LT));
+          const int64_t tq = base + q < T ? base + q : T - 1;
+          const uint32_t keep = exact_groups(logits + tq * E, bias, E,
+                                             __shfl_sync(kAll, zmax, q * LT), o,
+                                             keys_s + warp * E);
+          __syncwarp();
+          if (tw == q) kept = in && ((keep >> g) & 1u);
+        }
       }
       if (!kept) {
 #pragma unroll
@@ -469,6 +491,7 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
     // k-th: ``count`` of them then.  ``near``: a gap between two was too narrow to
     // tell their order.
     const int cand = d.groups > 1 ? o.topk_group * d.size : E;
+    bool all_again = false;  // the whole choice has to be made on fp64 values
     auto pop = [&](int r, uint32_t top) {
       const uint32_t b = __ballot_sync(kAll, a[0] == top);
       if (a[0] == top && !(b & below) && top) {
