@@ -269,7 +269,8 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
   const uint32_t sA = base;
   const uint32_t sB = base + p.stages * kABytes;
   volatile int32_t* abort_flag = &ctl->abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the warp index by a shuffle, so that the compiler knows it is one per warp)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = (CG == 2 || SPLIT > 1) ? cluster_ctarank() : 0u;
 
   if (threadIdx.x == 0) {
@@ -310,23 +311,22 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, filled = 0, last = 0;  // bit s: stage s filled, its parity
-      bool ok = true;
-      for (uint32_t u = unit0; ok && u < total; u += step) {
-        const LinTile tl = lin_tile(u, p);
-        const int mrow = (tl.mt * CG + (int)(CG == 2 ? rank : 0)) * (GATED ? 64 : 128);
-        const int64_t tr = tl.t0 + (CG == 2 ? (int64_t)rank * (p.tn / 2) : 0);
-        // each weight tile starts elsewhere in K and wraps round (integer sums
-        // do not mind), so that the CTAs do not all read the same lines of x
-        // at the same time
-        int kb = kb0 + (int)(tl.mt * 5u % (uint32_t)(kb1 - kb0));
-        for (int i = kb0; i < kb1; ++i, kb = kb + 1 < kb1 ? kb + 1 : kb0) {
-          if (!wait_for(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0, filled = 0, last = 0;  // bit s: stage s filled, its parity
+    bool ok = true;
+    for (uint32_t u = unit0; ok && u < total; u += step) {
+      const LinTile tl = lin_tile(u, p);
+      const int mrow = (tl.mt * CG + (int)(CG == 2 ? rank : 0)) * (GATED ? 64 : 128);
+      const int64_t tr = tl.t0 + (CG == 2 ? (int64_t)rank * (p.tn / 2) : 0);
+      // each weight tile starts elsewhere in K and wraps round (integer sums
+      // do not mind), so that the CTAs do not all read the same lines of x
+      // at the same time
+      int kb = kb0 + (int)(tl.mt * 5u % (uint32_t)(kb1 - kb0));
+      for (int i = kb0; i < kb1; ++i, kb = kb + 1 < kb1 ? kb + 1 : kb0) {
+        ok = __all_sync(0xffffffffu,
+                        wait_for(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err));
+        if (!ok) break;
+        if (elect_one()) {
           uint32_t fb = smem_u32(&ctl->full[stage]);
           // with a pair both CTAs' bytes complete on CTA 0's barrier
           if (CG == 1 || rank == 0) mbar_expect_tx(fb, CG * (kABytes + b_bytes));
@@ -353,23 +353,27 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
             else
               tma_load_2d(b + s * sub_bytes, &tmX, kx, (int32_t)(tr + s * p.tn), fb);
           }
-          filled |= 1u << stage;
-          last = (last & ~(1u << stage)) | (phase << stage);
-          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
         }
-      }
-      if (!ok && (CG == 1 || rank == 0)) {
-        // let the copies already issued land before the block exits
-        int32_t none = 0;
-        volatile int32_t* never = &none;
-        for (int s = 0; s < p.stages; ++s)
-          if ((filled >> s) & 1u)
-            mbar_wait(smem_u32(&ctl->full[s]), (last >> s) & 1u, never, kTimeoutNs, p.err);
+        __syncwarp();
+        filled |= 1u << stage;
+        last = (last & ~(1u << stage)) | (phase << stage);
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
       }
     }
+    if (!ok && lane == 0 && (CG == 1 || rank == 0)) {
+      // let the copies already issued land before the block exits
+      int32_t none = 0;
+      volatile int32_t* never = &none;
+      for (int s = 0; s < p.stages; ++s)
+        if ((filled >> s) & 1u)
+          mbar_wait(smem_u32(&ctl->full[s]), (last >> s) & 1u, never, kTimeoutNs, p.err);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
-    if (lane == 0 && (CG == 1 || rank == 0)) {
+    // The whole warp walks the k-blocks and one lane issues (elect_one): an MMA of up to
+    // 192 columns would otherwise take longer to issue than to run.
+    if (CG == 1 || rank == 0) {
       const uint32_t idesc = idesc_i8_s32(128 * CG, p.tn);
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
@@ -378,46 +382,59 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
         const uint32_t eb = smem_u32(&ctl->tmem_empty[buf]);
         ok = CG == 2 ? wait_for_cluster(eb, buf_phase ^ 1u, abort_flag, p.err)
                      : wait_for(eb, buf_phase ^ 1u, abort_flag, p.err);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * 256;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_for(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu,
+                          wait_for(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err));
+          if (!ok) break;
           tc_fence_after();
           const uint64_t ad = sw128_kmajor_desc(sA + stage * kABytes);
-          for (int s = 0; s < p.nsub; ++s) {
-            const uint64_t bd = sw128_kmajor_desc(sB + stage * b_bytes + s * sub_bytes);
-            // four MMAs of 32 bytes of K each
+          const uint64_t bd = sw128_kmajor_desc(sB + stage * b_bytes);
+          const uint32_t first = kb != kb0 ? 1u : 0u;
+          if (elect_one()) {
+            // four MMAs of 32 bytes of K each for each sub-tile
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_i8<CG>(d + s * 256, ad + 2u * kk, bd + 2u * kk, idesc,
-                          (kb != kb0 || kk != 0) ? 1u : 0u);
+              umma_i8<CG>(d, ad + 2u * kk, bd + 2u * kk, idesc, first | (kk != 0));
+            if (p.nsub == 2) {
+              const uint64_t b2 = bd + (sub_bytes >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_i8<CG>(d + 256, ad + 2u * kk, b2 + 2u * kk, idesc, first | (kk != 0));
+            }
+            if (CG == 2)
+              umma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
+            else
+              umma_commit(smem_u32(&ctl->empty[stage]));
           }
-          if (CG == 2)
-            umma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
-          else
-            umma_commit(smem_u32(&ctl->empty[stage]));
+          __syncwarp();
           if (++stage == p.stages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        if (CG == 2)
-          umma_commit_pair_mc(smem_u32(&ctl->tmem_full[buf]), 0x3);
-        else
-          umma_commit(smem_u32(&ctl->tmem_full[buf]));
+        if (elect_one()) {
+          if (CG == 2)
+            umma_commit_pair_mc(smem_u32(&ctl->tmem_full[buf]), 0x3);
+          else
+            umma_commit(smem_u32(&ctl->tmem_full[buf]));
+        }
+        __syncwarp();
         if (++buf == p.nbuf) { buf = 0; buf_phase ^= 1u; }
       }
-      if (!ok || *abort_flag) {
+      if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
         // wait for the MMAs already issued before TMEM is released
-        int32_t none = 0;
-        volatile int32_t* never = &none;
-        if (CG == 2)
-          umma_commit_pair(smem_u32(&ctl->drain));
-        else
-          umma_commit(smem_u32(&ctl->drain));
-        mbar_wait(smem_u32(&ctl->drain), 0, never, kTimeoutNs, p.err);
+        if (elect_one()) {
+          int32_t none = 0;
+          volatile int32_t* never = &none;
+          if (CG == 2)
+            umma_commit_pair(smem_u32(&ctl->drain));
+          else
+            umma_commit(smem_u32(&ctl->drain));
+          mbar_wait(smem_u32(&ctl->drain), 0, never, kTimeoutNs, p.err);
+        }
+        __syncwarp();
       }
     }
   } else {

