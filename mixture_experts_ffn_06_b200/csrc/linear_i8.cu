@@ -35,6 +35,7 @@ constexpr int kABytes = 128 * 128;   // 128 weight rows x 128 bytes of K
 constexpr int kMaxStages = 12;
 constexpr uint64_t kTimeoutNs = 1000000000ull;  // 1 s per wait
 constexpr int kSmemMax = 227 * 1024;
+constexpr int kScaleBytes = 4096;  // token scales of the epilogue warps, at most
 constexpr int kMaxDev = 64;
 
 struct LinParams {
@@ -256,10 +257,10 @@ __global__ void __launch_bounds__(64 + 32 * EW, 1)
 linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmX, const LinParams p) {
   static_assert(CG == 1 || SPLIT == 1, "K is split over single CTAs");
-  static_assert(EW == 4 || EW == 8, "one or two warps for each 32 accumulator lanes");
+  static_assert(EW == 4 || EW == 8 || EW == 16, "whole warps for each 32 accumulator lanes");
   extern __shared__ uint8_t smem_raw[];
   __shared__ LinCtl ctl_s;
-  __shared__ __align__(16) float sx_s[EW][32];
+  __shared__ __align__(16) float sx_s[SPLIT == 1 ? EW : 1][EW == 4 ? 4 : 32 / EW][32];
   LinCtl* ctl = &ctl_s;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -439,10 +440,11 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
     }
   } else {
     // ----------------------------------------------------------- epilogue
-    // Warp w reads TMEM lanes [32 (w % 4), 32 (w % 4) + 32); with eight warps,
-    // two take the 32-column chunks of the same lanes in turn.
+    // Warp w reads TMEM lanes [32 (w % 4), 32 (w % 4) + 32); the EW / 4 warps of the
+    // same lanes take their 32-column chunks in turn.
     const int q = warp & 3;
     constexpr int HALVES = EW / 4;
+    constexpr int CHUNKS = EW == 4 ? 4 : 8 / HALVES;  // of a warp (EW = 4: tn <= 128)
     const int c_first = 32 * ((warp - 2) >> 2);
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t empty0 = CG == 2 ? mapa_shared(smem_u32(&ctl->tmem_empty[0]), 0) : 0u;
@@ -453,16 +455,19 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
       const LinTile tl = lin_tile(u, p);
       LaneOut<GATED> lo;
       lo.init(p, (tl.mt * CG + (int)(CG == 2 ? rank : 0)) * 128 + q * 32 + lane, lane);
-      // token scales of this warp's chunks, requested before the wait
-      float sl[4];
+      // Token scales of this warp's chunks, brought to shared memory before the wait
+      // and by the parity of their token: a lane reads the 16 of its own columns of
+      // a chunk as four vectors.
       auto token_scales = [&](int64_t ts) {
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < CHUNKS; ++i) {
           const int64_t tok = ts + c_first + 32 * HALVES * i + lane;
-          sl[i] = tok < p.T ? __ldg(p.xs + tok) : 0.f;
+          sx_s[warp - 2][i][(lane & 1) * 16 + (lane >> 1)] = tok < p.T ? __ldg(p.xs + tok) : 0.f;
         }
+        __syncwarp();
       };
-      if (SPLIT == 1) token_scales(tl.t0);
+      if constexpr (SPLIT == 1) token_scales(tl.t0);
       const bool got = wait_for(smem_u32(&ctl->tmem_full[buf]), buf_phase, abort_flag, p.err);
       // warp-uniform decision; also reconverges the warp for tcgen05.ld
       if (!__all_sync(0xffffffffu, got)) break;
@@ -480,23 +485,18 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
             if (c + j < p.tn) part[(c + j) * 128] = (int32_t)v[j];
         }
       } else {
-        float* sx_w = sx_s[warp - 2];
         for (int s = 0; s < p.nsub; ++s) {
           const int64_t ts = tl.t0 + (int64_t)s * p.tn;
           // columns past tn belong to the next sub-tile or to nobody
           const int64_t t_end = ts + p.tn < p.T ? ts + p.tn : p.T;
           if (s > 0) token_scales(ts);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < CHUNKS; ++i) {
             const int c = c_first + 32 * HALVES * i;
             if (c >= p.tn || ts + c >= p.T) break;
             uint32_t v[32];
             tmem_ld32(tb + s * 256 + c, v);
-            // the scales by the parity of their token: a lane reads the 16 of its
-            // own columns as four vectors
-            __syncwarp();
-            sx_w[(lane & 1) * 16 + (lane >> 1)] = sl[i];
-            __syncwarp();
+            const float* sx_w = sx_s[warp - 2][i];
 #pragma unroll
             for (int h = 0; h < 32; h += 16) {
               int32_t a[8], b[8];
@@ -740,7 +740,7 @@ cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, 
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev || !ready[dev].load()) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemMax - (int)(sizeof(LinCtl) + sizeof(float) * 32 * EW));
+                             kSmemMax - (int)sizeof(LinCtl) - kScaleBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDev) ready[dev].store(true);
   }
@@ -772,11 +772,15 @@ cudaError_t launch_few(const LinParams& p, int blocks, const int8_t* x, const in
                    reinterpret_cast<const int4*>(x), reinterpret_cast<const int4*>(w), K / 16, p);
 }
 
-// The tile of the many-token form: the one with the least estimated time.  Per
-// k-block an SM (or each SM of a pair) takes about max(360, 180 + 1.1 c) ns for c
-// token columns (measured on B200, c = 64 to 512: 365 ns up to 128, 390 at 192, 430
-// at 256, 515 at 320, 740 at 512); a tile's epilogue about 1000 + 14 c ns, which
-// runs beside the next tile's MMAs while two accumulators fit (c <= 256).
+// The tile of the many-token form: the one with the least estimated time, from what
+// was measured on B200 for c token columns (c = 64 to 512) in ns.  A k-block takes an
+// SM of a pair max(200 + 0.27 c, 90 + 0.86 c) (217 at 64, 255 at 192, 310 at 256) and a
+// single CTA max(245 + 0.2 c, 135 + 0.86 c) (258, 300, 355), which loads all of a
+// token tile where each CTA of a pair loads half; a pair takes 900 more to start.  A
+// tile's epilogue takes about 1000 + 7 c beside the next tile's MMAs, while two
+// accumulators fit (c <= 256), and 1500 + 10 c after its own.  T = 512, K = 4096, N = 14336: pairs of 256 columns 26.7 us,
+// singles 29.9, pairs of 2 x 256 30.4; T = 512, K = 2816, 2 x 2112 gated: singles of 128
+// 10.7, pairs 10.9, pairs of 256 13.9.
 struct LinPlan {
   int cg, tn, nsub, TT;
   double ns;
@@ -784,32 +788,23 @@ struct LinPlan {
 
 LinPlan plan_tiles(int64_t T, int mt128, int KB, int sms) {
   LinPlan best{1, 0, 0, 0, 0.0};
-  for (int nsub = 1; nsub <= 2; ++nsub) {
-    const int tt0 = ceil_div(T, 256 * nsub);
-    for (int tt = tt0; tt <= tt0 + 4; ++tt) {
-      const int per = ceil_div(T, (int64_t)tt * nsub);
-      // CTA pairs halve what each SM loads of the tokens: worth their start-up over
-      // several rounds (loops of the same call, under the power limit: K = 4096, T =
-      // 4096 401 against 415 us; K = 2816, T = 8192 95 against 98; one round, K =
-      // 2816, T = 512: 14.3 against 13.1) and for 512 columns (T = 512: 31 against 36)
-      int cg = 1;
-      int64_t rounds = 0;
-      int tn = 0, TT = 0;
-      for (;;) {
-        tn = 16 * cg * ceil_div(per, 16 * cg);
-        TT = ceil_div(T, (int64_t)tn * nsub);
-        rounds = (ceil_div(mt128, cg) * (int64_t)TT + sms / cg - 1) / (sms / cg);
-        if (cg == 1 && (rounds >= 4 || nsub * tn > 384)) cg = 2;
-        else break;
+  for (int cg = 1; cg <= 2; ++cg)
+    for (int nsub = 1; nsub <= 2; ++nsub) {
+      const int tt0 = ceil_div(T, 256 * nsub);
+      for (int tt = tt0; tt <= tt0 + 4; ++tt) {
+        const int tn = 16 * cg * ceil_div(ceil_div(T, (int64_t)tt * nsub), 16 * cg);
+        const int TT = ceil_div(T, (int64_t)tn * nsub);
+        const int64_t rounds = (ceil_div(mt128, cg) * (int64_t)TT + sms / cg - 1) / (sms / cg);
+        const double c = (double)tn * nsub;
+        const double body = KB * (cg == 1 ? std::max(245.0 + 0.2 * c, 135.0 + 0.86 * c)
+                                          : std::max(200.0 + 0.27 * c, 90.0 + 0.86 * c));
+        const double epi = nsub == 1 ? 1000.0 + 7.0 * c : 1500.0 + 10.0 * c;
+        const double ns = (cg == 2 ? 900.0 : 0.0) +
+                          (nsub == 1 ? (rounds - 1) * std::max(body, epi) + body + epi
+                                     : rounds * (body + epi));
+        if (best.tn == 0 || ns < best.ns) best = LinPlan{cg, tn, nsub, TT, ns};
       }
-      if (tn > 256) continue;
-      const double c = (double)tn * nsub;
-      const double body = KB * std::max(360.0, 180.0 + 1.1 * c), epi = 1000.0 + 14.0 * c;
-      const double ns = nsub == 1 ? (rounds - 1) * std::max(body, epi) + body + epi
-                                  : rounds * (body + epi);
-      if (best.tn == 0 || ns < best.ns) best = LinPlan{cg, tn, nsub, TT, ns};
     }
-  }
   return best;
 }
 
@@ -848,7 +843,7 @@ cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cud
     // all CTAs resident at once where two or three fit an SM
     const int res = std::min(3, ceil_div((int64_t)mt128 * split, sms));
     const int stage = kABytes + p.tn * 128;
-    p.stages = std::min({kMaxStages, (kSmemMax / res - 3 * 1024) / stage, ceil_div(p.KB, split)});
+    p.stages = std::min({kMaxStages, (kSmemMax / res - 4 * 1024) / stage, ceil_div(p.KB, split)});
     if (split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, mt128, st);
     if (split == 2) return launch_linear<1, GATED, 2, 8>(p, x, w, K, mt128, st);
     if (split == 4) return launch_linear<1, GATED, 4, 8>(p, x, w, K, mt128, st);
@@ -863,12 +858,12 @@ cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cud
   p.MT = ceil_div(mt128, pl.cg);
   p.cols = 512;
   const int stage = kABytes + p.tn / pl.cg * 128 * p.nsub;
-  p.stages = std::min(kMaxStages, (kSmemMax - 3 * 1024) / stage);
+  p.stages = std::min(kMaxStages, (kSmemMax - 6 * 1024) / stage);
   const int64_t tiles = (int64_t)p.MT * p.TT;
   if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   if (pl.cg == 1)
-    return launch_linear<1, GATED, 1, 8>(p, x, w, K, (int)std::min<int64_t>(sms, tiles), st);
-  return launch_linear<2, GATED, 1, 8>(p, x, w, K, (int)std::min<int64_t>(sms / 2, tiles), st);
+    return launch_linear<1, GATED, 1, 16>(p, x, w, K, (int)std::min<int64_t>(sms, tiles), st);
+  return launch_linear<2, GATED, 1, 16>(p, x, w, K, (int)std::min<int64_t>(sms / 2, tiles), st);
 }
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -87,7 +87,8 @@ def test_gated_product(api, T, N, K, act):
 # weight tile on single CTAs and on pairs
 FORMS = [(8, 14336, 64), (3, 20000, 48), (12, 9000, 128), (40, 20000, 128), (700, 14000, 640),
          (600, 14336, 256), (2000, 16384, 256), (257, 14336, 2064), (512, 18944, 2704),
-         (1024, 18944, 4112), (1030, 18944, 2704), (5000, 640, 1040)]
+         (1024, 18944, 4112), (1030, 18944, 2704), (5000, 640, 1040),
+         (512, 18944, 8192), (1024, 18944, 8192)]
 
 
 @pytest.mark.parametrize("T,N,K", FORMS)
