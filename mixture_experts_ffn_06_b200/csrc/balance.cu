@@ -653,10 +653,11 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
   const int64_t T = shape->T;
   const bool vec = ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0;
   // A warp per token while that leaves the SMs room; else the fewest lanes that the
-  // groups and 32 experts a lane allow.
+  // groups and 32 experts a lane allow (E = 64, device time with 32 lanes and with 8:
+  // T = 1300 4.6 and 6.1 us, T = 4095 6.9 and 6.8, T = 8192 10.6 and 8.3).
   int LT = 32;
   Deal d = deal(E, o.n_group, 32, vec);
-  if (k <= 8 && T > 8 * device_sm_count()) {
+  if (k <= 8 && T > 24 * device_sm_count()) {
     for (int lt = 8; lt < 32; lt *= 2) {
       const Deal c = deal(E, o.n_group, lt, vec);
       if (c.n > 32) continue;

@@ -83,19 +83,19 @@ def test_matches_the_definition(api, case, with_bias):
 
 # many tokens: 8 or 16 lanes to a token, experts read in quads or one by one
 MANY = [
-    (1301, 8, 2, 0, 1, 1, 1, True, 1.0),
-    (1301, 64, 6, 0, 1, 1, 1, False, 1.0),
-    (1303, 66, 8, 1, 1, 1, 1, True, 1.0),
-    (1200, 128, 8, 1, 1, 1, 1, True, 1.0),
-    (1300, 256, 8, 1, 8, 4, 2, True, 2.5),
-    (1300, 250, 8, 0, 1, 1, 1, True, 1.0),
-    (1300, 256, 8, 0, 4, 3, 1, False, 1.0),
-    (1300, 512, 8, 1, 1, 1, 1, True, 1.0),
-    (1300, 500, 7, 1, 5, 2, 2, True, 1.0),
-    (1300, 96, 8, 1, 3, 1, 2, True, 1.0),
-    (1300, 160, 6, 0, 16, 5, 2, True, 1.0),
-    (1300, 510, 8, 1, 17, 9, 2, True, 1.0),
-    (1300, 128, 12, 0, 1, 1, 1, True, 1.0),
+    (3701, 8, 2, 0, 1, 1, 1, True, 1.0),
+    (3701, 64, 6, 0, 1, 1, 1, False, 1.0),
+    (3703, 66, 8, 1, 1, 1, 1, True, 1.0),
+    (3600, 128, 8, 1, 1, 1, 1, True, 1.0),
+    (3700, 256, 8, 1, 8, 4, 2, True, 2.5),
+    (3700, 250, 8, 0, 1, 1, 1, True, 1.0),
+    (3700, 256, 8, 0, 4, 3, 1, False, 1.0),
+    (3700, 512, 8, 1, 1, 1, 1, True, 1.0),
+    (3700, 500, 7, 1, 5, 2, 2, True, 1.0),
+    (3700, 96, 8, 1, 3, 1, 2, True, 1.0),
+    (3700, 160, 6, 0, 16, 5, 2, True, 1.0),
+    (3700, 510, 8, 1, 17, 9, 2, True, 1.0),
+    (3700, 128, 12, 0, 1, 1, 1, True, 1.0),
     (20000, 32, 4, 1, 1, 1, 1, True, 1.0),
 ]
 
@@ -105,7 +105,7 @@ def test_many_tokens(api, case):
     test_matches_the_definition(api, case, True)
 
 
-@pytest.mark.parametrize("T", [40, 1300])
+@pytest.mark.parametrize("T", [40, 3700])
 @pytest.mark.parametrize("scoring", [0, 1])
 @pytest.mark.parametrize("spread", [0.0, 1e-7, 1e-3])
 def test_the_largest_together(api, T, scoring, spread):
@@ -123,12 +123,32 @@ def test_the_largest_together(api, T, scoring, spread):
         _check(_run(api, z, k, **opts), ref.route(z, k, **opts))
 
 
+@pytest.mark.parametrize("T", [70, 3700])
+@pytest.mark.parametrize("off_logits,off_bias", [(1, 0), (0, 3), (2, 1)])
+def test_rows_off_a_16_byte_boundary(api, T, off_logits, off_bias):
+    g = np.random.default_rng(29)
+    E, k = 256, 8
+    z = g.standard_normal((T, E)).astype(np.float32)
+    bias = (0.1 * g.standard_normal(E)).astype(np.float32)
+    zd = torch.zeros(T * E + 4, device="cuda")[off_logits:off_logits + T * E].view(T, E)
+    bd = torch.zeros(E + 4, device="cuda")[off_bias:off_bias + E]
+    zd.copy_(torch.from_numpy(z))
+    bd.copy_(torch.from_numpy(bias))
+    opts = dict(scoring=1, n_group=8, topk_group=4, group_top=2)
+    ids = torch.full((T, k), -5, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), float("nan"), device="cuda")
+    load = torch.full((E,), -5, dtype=torch.int32, device="cuda")
+    api.moe_route_balanced(api.make_shape(T=T, H=8, E=E, k=k, I=8), zd, bd, None, ids, w,
+                           load=load, opts=api.balance_opts(**opts))
+    _check((ids, w, load), ref.route(z, k, bias, None, **opts))
+
+
 def test_defaults_without_options_and_load(api):
     z = np.random.default_rng(0).standard_normal((50, 24)).astype(np.float32)
     _check(_run(api, z, 3, with_load=False), ref.route(z, 3))
 
 
-@pytest.mark.parametrize("T", [300, 1300])
+@pytest.mark.parametrize("T", [300, 3700])
 @pytest.mark.parametrize("scoring", [0, 1])
 def test_close_choices_are_ranked_as_real_numbers(api, scoring, T):
     # scores that fp32 cannot tell apart: logits one ulp apart, with biases that
@@ -151,7 +171,7 @@ def test_close_choices_are_ranked_as_real_numbers(api, scoring, T):
 
 @pytest.mark.parametrize("n_group,topk_group,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
 @pytest.mark.parametrize("scoring", [0, 1])
-@pytest.mark.parametrize("T", [200, 1300])
+@pytest.mark.parametrize("T", [200, 3700])
 def test_equal_values_go_to_the_lower_id(api, T, scoring, n_group, topk_group, group_top):
     g = np.random.default_rng(6)
     z = g.integers(-1, 2, (T, 48)).astype(np.float32)  # many equal logits
@@ -165,7 +185,7 @@ def test_equal_values_go_to_the_lower_id(api, T, scoring, n_group, topk_group, g
 @pytest.mark.parametrize("n_group,topk_group,group_top", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
 @pytest.mark.parametrize("scoring", [0, 1])
 @pytest.mark.parametrize("renorm", [True, False])
-@pytest.mark.parametrize("T", [40, 1300])
+@pytest.mark.parametrize("T", [40, 3700])
 def test_masked_and_special_logits(api, T, scoring, renorm, n_group, topk_group, group_top):
     g = np.random.default_rng(7)
     E, k = 64, 6
