@@ -494,18 +494,20 @@ def moe_quantize_rows_i8(src, codes, scales, stream=None):
 def moe_linear_i8(x, x_scale, w, w_scale, out, ws, gate_act=None, out_f32=None, stream=None):
     """The int8 product x [T,K] @ w [N,K]^T with scales per token and per channel
     into ``out`` [T,N] bf16 (or None) and ``out_f32`` [T,N] fp32 (or None).
-    ``gate_act`` None, or ACT_SILU / ACT_GELU_TANH: w holds gate rows, then up
+    ``gate_act`` None (LINEAR_PLAIN), or ACT_SILU / ACT_GELU_TANH: w holds gate rows, then up
     rows, and out is [T,N/2] = Act(gate) * up.  ``ws``: at least 256 bytes
     (uint8), zeroed once; its error word is read by moe_read_error."""
     T, K = x.shape
     N = w.shape[0]
+    if gate_act is None:
+        gate_act = LINEAR_PLAIN
     d, i8, f32 = _dev(x), torch.int8, torch.float32
-    n_out, n_ws = T * (N if gate_act is None else N // 2), ws.numel()
+    n_out, n_ws = T * (N if gate_act == LINEAR_PLAIN else N // 2), ws.numel()
     st = lib.moe_linear_i8(
         T, N, K, _q(x, i8, T * K, d, "x"), _q(x_scale, f32, T, d, "x_scale"),
         _q(w, i8, N * K, d, "w"), _q(w_scale, f32, N, d, "w_scale"),
-        LINEAR_PLAIN if gate_act is None else gate_act,
-        _q(out, torch.bfloat16, n_out, d, "out"), _q(out_f32, f32, n_out, d, "out_f32"),
+        gate_act, _q(out, torch.bfloat16, n_out, d, "out"),
+        _q(out_f32, f32, n_out, d, "out_f32"),
         _q(ws, torch.uint8, n_ws, d, "ws"), n_ws,
         _cuda_stream(d) if stream is None else stream.cuda_stream)
     if st:

@@ -151,6 +151,22 @@ def test_one_output_at_a_time(api, T, N, K, act):
     assert torch.equal(_run(api, x, xs, w, ws, act, bf16=False)[1], o32)
 
 
+def test_the_plain_constant_is_the_plain_product(api):
+    T, N, K = 5, 48, 64
+    x, xs, w, ws = _inputs(T, N, K, 17)
+    assert torch.equal(_run(api, x, xs, w, ws, fp32=False)[0],
+                       _run_plain_constant(api, x, xs, w, ws, N))
+    with pytest.raises(ValueError, match="out: expected"):
+        _run_plain_constant(api, x, xs, w, ws, N // 2)  # room for a gated product alone
+
+
+def _run_plain_constant(api, x, xs, w, ws, n):
+    out = torch.zeros(x.shape[0], n, dtype=torch.bfloat16, device="cuda")
+    api.moe_linear_i8(*[torch.from_numpy(v).cuda() for v in (x, xs, w, ws)], out, _ws(),
+                      gate_act=api.LINEAR_PLAIN)
+    return out
+
+
 class Guarded:
     """A buffer between two bands of a known byte."""
 
