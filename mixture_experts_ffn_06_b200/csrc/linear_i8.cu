@@ -10,16 +10,19 @@
 // each epilogue warp, 16 gate rows and then the matching 16 up rows (one 3D
 // TMA box over w [2, I, K]), so lane l's partner is lane l + 16.
 //
-// The fewest tokens take a form of small independent blocks
-// (linear_i8_few_kernel below).  The others, both with one TMA warp, one MMA warp and four epilogue warps:
-//   up to 128 tokens (bound by streaming w): a tile per cluster of up to 8 CTAs that
+// Which form runs depends on what bounds it (run_linear at the end has the rules):
+//   few tokens, streaming w: small independent blocks with mma.sync
+//               (linear_i8_few_kernel);
+//   fewer tiles than SMs and K long enough: a tile per cluster of up to 8 CTAs that
 //               split K; each parks its partial sums in shared memory and adds
 //               up a slice of the columns over all CTAs' (integers: the order
 //               of the sum does not matter);
+//   up to 128 tokens otherwise, streaming w: a CTA per tile, two or three to an SM;
 //   more (bound by the tensor cores, under the power limit): persistent CTAs or
 //               CTA pairs (M = 256) walk the tiles, two accumulators in TMEM so
 //               that a tile's epilogue runs beside the next one's MMAs, or one of
 //               twice the columns, which reads each weight tile half as often.
+// The tcgen05 forms have one TMA warp, one MMA warp and 4, 8 or 16 epilogue warps.
 // Every mbarrier wait is bounded (tc_ptx.cuh); after a timeout the block
 // records MOE_ERR_TIMEOUT, waits for its own copies and MMAs and frees TMEM.
 #include <algorithm>
@@ -162,7 +165,8 @@ struct LaneOut {
 
   // NP pairs of columns of this lane's row: a[j], b[j] are columns of tokens
   // t + stride j and t + stride j + 1 (tokens from t_end on are not stored),
-  // sx[j] the scale of the one this lane finishes.  No branch between the pairs, so that their chains overlap.
+  // sx[j] the scale of the one this lane finishes.  No branch between the pairs, so
+  // that their chains overlap.
   template <int NP>
   __device__ __forceinline__ void store(const LinParams& p, int64_t t, int64_t t_end, int stride,
                                         const int32_t (&a)[NP], const int32_t (&b)[NP],
@@ -250,8 +254,11 @@ struct LaneOut {
   }
 };
 
-// CG = 2: CTA pairs walk the tiles.  CG = 1: one tile per cluster of SPLIT CTAs
-// that share K.  EW epilogue warps.
+// CG = 2: CTA pairs walk the tiles.  CG = 1: single CTAs do, or with SPLIT > 1 a cluster
+// of SPLIT CTAs that share K takes one tile.  EW epilogue warps: 16 beside the MMAs of
+// the next tile (gated 1408 x 2816, T = 16384: 53 us, with eight 59), 8 where sums are
+// handed over (2112 x 2816, T = 128: 6.9 us, with four 7.3), 4 where several CTAs share
+// an SM.
 template <int CG, bool GATED, int SPLIT, int EW>
 __global__ void __launch_bounds__(64 + 32 * EW, 1)
 linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
@@ -544,6 +551,7 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
 #pragma unroll
       for (int r = 0; r < SPLIT; ++r) src[r] = mapa_shared(smem_u32(gbase) + row * 4, r);
       constexpr int GROUP = 2 * SPLIT * NP;  // columns of one turn, at most 32
+      const int64_t t_end = tl.t0 + p.tn < p.T ? tl.t0 + p.tn : p.T;
       for (int c0 = GROUP * half; c0 < p.tn && tl.t0 + c0 < p.T; c0 += GROUP * (EW / 4)) {
         const int c = c0 + 2 * (int)rank;
         int32_t a[NP], b[NP];
@@ -561,7 +569,7 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
           for (int j = 0; j < NP; ++j) {
             const uint32_t at = src[r] + (uint32_t)(c + 2 * SPLIT * j) * 512u;
             ua[j] = ub[j] = 0;
-            if (tl.t0 + c + 2 * SPLIT * j < p.T) {
+            if (tl.t0 + c + 2 * SPLIT * j < t_end) {
               ua[j] = ld_cluster_s32(at);
               ub[j] = ld_cluster_s32(at + 512u);
             }
@@ -572,7 +580,7 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
             b[j] += ub[j];
           }
         }
-        lo.template store<NP>(p, tl.t0 + c, p.T, 2 * SPLIT, a, b, sx);
+        lo.template store<NP>(p, tl.t0 + c, t_end, 2 * SPLIT, a, b, sx);
       }
     }
   }
@@ -726,6 +734,18 @@ cudaError_t make_gated_map(CUtensorMap* m, const void* ptr, uint64_t K, uint64_t
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+// The shared-memory opt-in of a kernel, once per device.
+template <int CG, bool GATED, int SPLIT, int EW>
+cudaError_t set_smem(int dev) {
+  static std::atomic<bool> ready[kMaxDev];
+  if (dev >= 0 && dev < kMaxDev && ready[dev].load()) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(linear_i8_kernel<CG, GATED, SPLIT, EW>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmemMax - (int)sizeof(LinCtl) - kScaleBytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDev) ready[dev].store(true);
+  return e;
+}
+
 template <int CG, bool GATED, int SPLIT, int EW>
 cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, int K,
                           int clusters, cudaStream_t st) {
@@ -734,16 +754,9 @@ cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, 
   cudaError_t e = GATED ? make_gated_map(&mw, w, K, p.NO) : make_tma_map_e4m3(&mw, w, K, p.N, 128);
   if (e == cudaSuccess) e = make_tma_map_e4m3(&mx, x, K, p.T, p.tn / CG);
   if (e != cudaSuccess) return e;
-  // the shared-memory opt-in is a per-device attribute
-  static std::atomic<bool> ready[kMaxDev];
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDev || !ready[dev].load()) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemMax - (int)sizeof(LinCtl) - kScaleBytes);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDev) ready[dev].store(true);
-  }
+  if ((e = set_smem<CG, GATED, SPLIT, EW>(dev)) != cudaSuccess) return e;
   constexpr int per = CG * SPLIT;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * per));
@@ -778,7 +791,8 @@ cudaError_t launch_few(const LinParams& p, int blocks, const int8_t* x, const in
 // single CTA max(245 + 0.2 c, 135 + 0.86 c) (258, 300, 355), which loads all of a
 // token tile where each CTA of a pair loads half; a pair takes 900 more to start.  A
 // tile's epilogue takes about 1000 + 7 c beside the next tile's MMAs, while two
-// accumulators fit (c <= 256), and 1500 + 10 c after its own.  T = 512, K = 4096, N = 14336: pairs of 256 columns 26.7 us,
+// accumulators fit (c <= 256), and 1500 + 10 c after its own.  T = 512, K = 4096,
+// N = 14336: pairs of 256 columns 26.7 us,
 // singles 29.9, pairs of 2 x 256 30.4; T = 512, K = 2816, 2 x 2112 gated: singles of 128
 // 10.7, pairs 10.9, pairs of 256 13.9.
 struct LinPlan {
@@ -808,46 +822,88 @@ LinPlan plan_tiles(int64_t T, int mt128, int KB, int sms) {
   return best;
 }
 
+// Clusters of SPLIT CTAs that run at once on the current device, a CTA to an SM.
+template <int SPLIT>
+int clusters_at_once() {
+  static std::atomic<int> known[kMaxDev];  // plus 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+  if (const int n = known[dev].load()) return n - 1;
+  auto kern = linear_i8_kernel<1, false, SPLIT, 8>;
+  const int smem = 128 * 1024;  // two do not fit an SM
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = SPLIT;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(SPLIT);
+  cfg.blockDim = dim3(64 + 32 * 8);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (set_smem<1, false, SPLIT, 8>(dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess)
+    return 0;
+  known[dev].store(n + 1);
+  return n;
+}
+
 template <bool GATED>
 cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cudaStream_t st) {
   const int sms = device_sm_count();
   const int rows = GATED ? 64 : 128;  // output channels of 128 weight rows
   // Sixteen warps to a block while three blocks or fewer come to an SM, so that
-  // enough loads are in flight (gated 2816 x 4224, T = 1: 3.6 us, with eight 5.6;
-  // 4096 x 28672: 25.9 us, with eight 20.2).  A second tile of tokens pays for small
-  // weights alone, since every block reads all tokens (2816 x 4224, T = 16: 5.1 us
-  // against 6.3 on the tcgen05 form; 4096 x 14336: 19 against 13.7; 14336 x 4096: 17.1
-  // against 14.1).
+  // enough loads are in flight (gated 2816 x 4224, T = 1: 3.6 us, with eight 5.9;
+  // gated 4096 x 28672: 25.9 us, with eight 20.2).  A second tile of tokens pays for small
+  // weights alone, since every block reads all tokens (gated 2816 x 4224, T = 16: 5.1 us
+  // against 5.6 on the tcgen05 forms, 2112 x 2816: 3.6 and 4.6; 4096 x 14336: 20.1 against
+  // 13.1; 14336 x 4096: 17.2 against 13.4).
   const int blocks = ceil_div(p.NO, GATED ? 8 : 16);
   if (p.T <= 8)
     return blocks <= 3 * sms ? launch_few<1, GATED, 16>(p, blocks, x, w, K, st)
                              : launch_few<1, GATED, 8>(p, blocks, x, w, K, st);
-  if (p.T <= 16 && blocks <= 2 * sms && K <= 4096) return launch_few<2, GATED, 16>(p, blocks, x, w, K, st);
+  if (p.T <= 16 && blocks <= 2 * sms && K <= 4096)
+    return launch_few<2, GATED, 16>(p, blocks, x, w, K, st);
   p.KB = ceil_div(K, 128);
   const int mt128 = ceil_div(p.NO, rows);
-  if (p.T <= 128) {
+  // Tiles of 128 weight rows and up to 128 tokens, K split as far as the clusters all
+  // run at once, a CTA to an SM (on B200 15 clusters of eight, 33 of four, 74 of two:
+  // not all SMs are in full clusters).  K = 8192, T = 64, in us with 1, 2, 4 and 8 CTAs:
+  // 14 tiles 19.1, 12.3, 8.5, 7.4; 16 tiles 19.1, 12.2, 8.6, 13.8; 36 tiles 19.3, 12.6,
+  // 18.0, 17.0; 80 tiles 20.2, 18.6, 29.8.  Handing the sums over costs as much as 5 k-blocks
+  // and one more for every 18 columns (4 tiles, T = 128, split and not: K = 1024 5.5
+  // and 4.6, K = 2048 5.7 and 6.4, K = 8192 7.2 and 16.7).
+  const int TT = ceil_div(p.T, 128), tn = 16 * ceil_div(ceil_div(p.T, TT), 16);
+  const int64_t small = (int64_t)mt128 * TT;
+  int split = 1;
+  if (small <= sms / 2) {
+    split = small <= clusters_at_once<8>() ? 8 : small <= clusters_at_once<4>() ? 4 : 2;
+    while (split > p.KB) split /= 2;
+    if (p.KB * (split - 1.0) / split <= 5.0 + tn / 18.0) split = 1;
+  }
+  // Unsplit tiles with several CTAs to an SM where there are more of them than SMs
+  // (T = 64, K = 2816: 150 tiles 12.4 us, on persistent CTAs 16.6; 300 tiles 22.1 and 24.3),
+  // and for the fewest tokens, whose short epilogue needs no sixteen warps (T = 17,
+  // K = 2816, 100 tiles: 9.4 and 10.2; T = 64: 10.1 and 9.9; T = 128: 12.0 and 10.4).
+  if (split > 1 || (p.T <= 128 && (mt128 > sms || p.T <= 32))) {
     p.nsub = 1;
-    p.tn = 16 * ceil_div(p.T, 16);
+    p.tn = tn;
     p.nbuf = 1;
-    p.TT = 1;
+    p.TT = ceil_div(p.T, tn);
     p.panel = 1;
     p.MT = mt128;
     p.cols = p.tn <= 32 ? 32 : p.tn <= 64 ? 64 : 128;
-    // K is split four ways at most while the SMs are half full by then or K is short:
-    // every CTA of a cluster reads the others' sums (2816 x 4224 gated, T = 64: 7.4 us
-    // with four, 8.6 with eight; 14336 x 4096, T = 17: 14.8 and 14.1)
-    int split = 1;
-    while (split < 8 && mt128 * split < sms && 2 * split <= p.KB &&
-           (split < 4 || 2 * mt128 * split <= sms || p.KB >= 64))
-      split *= 2;
-    // all CTAs resident at once where two or three fit an SM
-    const int res = std::min(3, ceil_div((int64_t)mt128 * split, sms));
-    const int stage = kABytes + p.tn * 128;
+    // without a split, all CTAs resident at once where two or three fit an SM
+    const int res = split > 1 ? 1 : std::min(3, ceil_div(mt128, sms));
+    const int stage = kABytes + tn * 128;
     p.stages = std::min({kMaxStages, (kSmemMax / res - 4 * 1024) / stage, ceil_div(p.KB, split)});
-    if (split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, mt128, st);
-    if (split == 2) return launch_linear<1, GATED, 2, 8>(p, x, w, K, mt128, st);
-    if (split == 4) return launch_linear<1, GATED, 4, 8>(p, x, w, K, mt128, st);
-    return launch_linear<1, GATED, 8, 4>(p, x, w, K, mt128, st);
+    const int tiles = (int)p.MT * p.TT;
+    if (split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, tiles, st);
+    if (split == 2) return launch_linear<1, GATED, 2, 8>(p, x, w, K, tiles, st);
+    if (split == 4) return launch_linear<1, GATED, 4, 8>(p, x, w, K, tiles, st);
+    return launch_linear<1, GATED, 8, 8>(p, x, w, K, tiles, st);
   }
   const LinPlan pl = plan_tiles(p.T, mt128, p.KB, sms);
   p.tn = pl.tn;

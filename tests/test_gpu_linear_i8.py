@@ -88,7 +88,12 @@ def test_gated_product(api, T, N, K, act):
 FORMS = [(8, 14336, 64), (3, 20000, 48), (12, 9000, 128), (40, 20000, 128), (700, 14000, 640),
          (600, 14336, 256), (2000, 16384, 256), (257, 14336, 2064), (512, 18944, 2704),
          (1024, 18944, 4112), (1030, 18944, 2704), (5000, 640, 1040),
-         (512, 18944, 8192), (1024, 18944, 8192)]
+         (512, 18944, 8192), (1024, 18944, 8192),
+         # K split over clusters, with one token tile and several
+         (100, 130, 2064), (130, 130, 2064), (260, 514, 4112), (1025, 300, 2832), (390, 2500, 4112),
+         (1100, 780, 8192), (25, 4400, 8192), (128, 4500, 2064),
+         # fewer tiles than SMs, K too short to split
+         (20, 2000, 256), (100, 2000, 256), (128, 9000, 400)]
 
 
 @pytest.mark.parametrize("T,N,K", FORMS)
