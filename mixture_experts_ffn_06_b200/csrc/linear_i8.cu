@@ -854,18 +854,22 @@ template <bool GATED>
 cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cudaStream_t st) {
   const int sms = device_sm_count();
   const int rows = GATED ? 64 : 128;  // output channels of 128 weight rows
-  // Sixteen warps to a block while three blocks or fewer come to an SM, so that
-  // enough loads are in flight (gated 2816 x 4224, T = 1: 3.6 us, with eight 5.9;
-  // gated 4096 x 28672: 25.9 us, with eight 20.2).  A second tile of tokens pays for small
-  // weights alone, since every block reads all tokens (gated 2816 x 4224, T = 16: 5.1 us
-  // against 5.6 on the tcgen05 forms, 2112 x 2816: 3.6 and 4.6; 4096 x 14336: 20.1 against
-  // 13.1; 14336 x 4096: 17.2 against 13.4).
+  // The small blocks, each of which walks all of K: while K is short, with sixteen warps
+  // where at most two blocks come to an SM, which keeps enough loads in flight, else with
+  // eight while the blocks are few, or read weights in two places (gated).  In us with
+  // sixteen, with eight and on the tcgen05 forms, T = 1: gated 2816 x 4224 4.1, 6.1, 6.1;
+  // 4096 x 4096 5.8, 7.4, 6.9; 2048 x 8192 6.5, 5.6, 6.7; 3584 x 10000 12.4, 8.6, 10.1;
+  // 4096 x 14336 16.7, 15.2, 12.9; gated 4096 x 14336 15.4, 12.1, 13.6; gated 4096 x 28672
+  // 26.0, 20.2, 21.1; 8192 x 1024 7.2, 12.2, 5.9; gated 8192 x 28672 45.7, 41.4, 38.3.  A
+  // second tile of tokens pays for small weights alone, since every block reads all
+  // tokens (T = 16, sixteen and tcgen05: gated 2816 x 4224 5.8 and 6.1, 2112 x 2816 4.2
+  // and 5.3, 4096 x 14336 20.1 and 12.9).
   const int blocks = ceil_div(p.NO, GATED ? 8 : 16);
-  if (p.T <= 8)
-    return blocks <= 3 * sms ? launch_few<1, GATED, 16>(p, blocks, x, w, K, st)
-                             : launch_few<1, GATED, 8>(p, blocks, x, w, K, st);
-  if (p.T <= 16 && blocks <= 2 * sms && K <= 4096)
-    return launch_few<2, GATED, 16>(p, blocks, x, w, K, st);
+  if (K <= 4096 && blocks <= 2 * sms && p.T <= 16)
+    return p.T <= 8 ? launch_few<1, GATED, 16>(p, blocks, x, w, K, st)
+                    : launch_few<2, GATED, 16>(p, blocks, x, w, K, st);
+  if (K <= 4096 && (GATED || blocks <= 5 * sms) && p.T <= 8)
+    return launch_few<1, GATED, 8>(p, blocks, x, w, K, st);
   p.KB = ceil_div(K, 128);
   const int mt128 = ceil_div(p.NO, rows);
   // Tiles of 128 weight rows and up to 128 tokens, K split as far as the clusters all

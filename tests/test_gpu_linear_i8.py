@@ -89,6 +89,8 @@ FORMS = [(8, 14336, 64), (3, 20000, 48), (12, 9000, 128), (40, 20000, 128), (700
          (600, 14336, 256), (2000, 16384, 256), (257, 14336, 2064), (512, 18944, 2704),
          (1024, 18944, 4112), (1030, 18944, 2704), (5000, 640, 1040),
          (512, 18944, 8192), (1024, 18944, 8192),
+         # few tokens: eight warps to a block, K too long for them, too many of them
+         (6, 5000, 4096), (8, 9000, 208), (1, 20000, 5008), (7, 200, 4112), (16, 20000, 64),
          # K split over clusters, with one token tile and several
          (100, 130, 2064), (130, 130, 2064), (260, 514, 4112), (1025, 300, 2832), (390, 2500, 4112),
          (1100, 780, 8192), (25, 4400, 8192), (128, 4500, 2064),
