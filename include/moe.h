@@ -481,9 +481,9 @@ MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const moe_bf16* x,
  * available experts comes after the others.  +inf counts as the largest
  * finite value.  A non-finite bias does the same to c (NaN as -inf).  The ids
  * of a token are always k different valid expert ids, whatever the row holds.
- * Uses no workspace; shape->H, I, n_shared, act are not read.  Bad options
- * return MOE_ERR_INVALID_ARG (MOE_ERR_UNSUPPORTED for n_group >
- * MOE_MAX_GROUPS) before any launch.
+ * Uses no workspace; shape->H, I, n_shared, act are validated and play no
+ * part.  Bad options return MOE_ERR_INVALID_ARG (MOE_ERR_UNSUPPORTED for
+ * n_group > MOE_MAX_GROUPS) before any launch.
  */
 typedef struct {
   int32_t scoring;     /* moe_scoring */

@@ -49,6 +49,7 @@ MAX_GROUPS = 32
 ACT_SILU, ACT_GELU_TANH = 0, 1
 LINEAR_PLAIN = -1
 LINEAR_MAX_K = 131056
+LINEAR_MAX_N = (1 << 22) - 1
 MAX_ROW = 32768
 
 
@@ -451,6 +452,13 @@ def _q(t, dtype, numel, dev, what):
     raise ValueError(f"{what}: expected a tensor on the current CUDA device, got {t.device}")
 
 
+def _within(n, most, where):
+    """A size that the library takes as an int: one past 32 bits would arrive there as
+    another."""
+    if n > most:
+        raise MoEError(2, where)
+
+
 def _dev(t):
     """The current CUDA device; a tensor elsewhere is refused by _q."""
     return _cuda_device() if t.is_cuda else 0
@@ -482,6 +490,7 @@ def moe_quantize_rows_i8(src, codes, scales, stream=None):
     """Per-row dynamic int8 quantisation of bf16 rows src [R, C] into codes
     (int8 [R, C]) and scales (fp32 [R])."""
     R, C = src.shape
+    _within(C, MAX_ROW, "moe_quantize_rows_i8")
     d = _dev(src)
     st = lib.moe_quantize_rows_i8(
         _q(src, torch.bfloat16, R * C, d, "src"), R, C, _q(codes, torch.int8, R * C, d, "codes"),
@@ -499,6 +508,8 @@ def moe_linear_i8(x, x_scale, w, w_scale, out, ws, gate_act=None, out_f32=None, 
     (uint8), zeroed once; its error word is read by moe_read_error."""
     T, K = x.shape
     N = w.shape[0]
+    _within(K, LINEAR_MAX_K, "moe_linear_i8")
+    _within(N, LINEAR_MAX_N, "moe_linear_i8")
     if gate_act is None:
         gate_act = LINEAR_PLAIN
     d, i8, f32 = _dev(x), torch.int8, torch.float32
@@ -523,6 +534,7 @@ def moe_block_norm(r, y=None, post_w=None, gate=None, token_gate=None, alpha=1.0
     [T,H] and scales [T].  post_w, pre_w and gate [H] bf16, token_gate [T]
     fp32.  r_out may be r."""
     T, H = r.shape
+    _within(H, MAX_ROW, "moe_block_norm")
     n, d, bf, f32 = T * H, _dev(r), torch.bfloat16, torch.float32
     prm = moe_block_norm_params(
         _q(y, bf, n, d, "y"), _q(r, bf, n, d, "r"), _q(post_w, bf, H, d, "post_w"),

@@ -161,3 +161,21 @@ def test_the_binding_refuses_wrong_tensors(api):
         api.moe_route_balanced(s, torch.zeros(4, 15), None, None, torch.zeros(4, 2), torch.zeros(4, 2))
     with pytest.raises(ValueError, match="x"):
         api.moe_linear_i8(r, torch.zeros(4), r, torch.zeros(4), r, torch.zeros(256, dtype=torch.uint8))
+
+
+def test_the_binding_refuses_sizes_past_32_bits(api):
+    # as a C int they would arrive as 16 (no memory behind these tensors)
+    def meta(dtype, *shape):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    big, i8, bf, f32 = (1 << 32) + 16, torch.int8, torch.bfloat16, torch.float32
+    ws = meta(torch.uint8, 256)
+    for call in (lambda: api.moe_linear_i8(meta(i8, 1, big), meta(f32, 1), meta(i8, 1, big),
+                                           meta(f32, 1), meta(bf, 1, 1), ws),
+                 lambda: api.moe_linear_i8(meta(i8, 1, 16), meta(f32, 1), meta(i8, big, 16),
+                                           meta(f32, big), meta(bf, 1, big), ws),
+                 lambda: api.moe_quantize_rows_i8(meta(bf, 1, big), meta(i8, 1, big), meta(f32, 1)),
+                 lambda: api.moe_block_norm(meta(bf, 1, big), pre_w=meta(bf, big), a=meta(bf, 1, big))):
+        with pytest.raises(api.MoEError) as e:
+            call()
+        assert e.value.status == 2
