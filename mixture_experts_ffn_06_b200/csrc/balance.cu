@@ -14,8 +14,11 @@
 // are few), each lane PER experts of one group: it sorts its values, packed with
 // their place in the low bits, by a network, so that a round of the top-k is a
 // maximum over the LT heads, and a group of one lane has its two largest in
-// front.  Bound by the instructions per expert (score and sort), then by
-// the k rounds; the bytes (4 E + 8 k per token) would take a tenth of the time.
+// front.  Bound by the instructions per expert (score and sort) and their latencies,
+// then by the k rounds; the bytes (4 E + 8 k per token) would take a fifteenth of
+// the time.  B200, device time: T = 16384, E = 64, k = 6 10.3 us (484 GB/s; 5.7 million warp
+// instructions, issued in 54 % of the cycles); T = 4095, E = 256, k = 8 in 8 groups
+// 10.6 us; T = 64, E = 128 4.5 us; T = 1, E = 256 in groups 5.1 us.
 #include <cfloat>
 #include <cmath>
 
@@ -651,7 +654,7 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
   }
   if (shape->T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
   const int64_t T = shape->T;
-  const bool vec = ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0;
+  const bool vec = aligned(logits, 16) && aligned(bias, 16);
   // A warp per token while that leaves the SMs room; else the fewest lanes that the
   // groups and 32 experts a lane allow (E = 64, device time with 32 lanes and with 8:
   // T = 1300 4.6 and 6.1 us, T = 4095 6.9 and 6.8, T = 8192 10.6 and 8.3).

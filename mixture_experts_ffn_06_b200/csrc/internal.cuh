@@ -232,6 +232,10 @@ cudaError_t make_tma_map_e4m3(CUtensorMap* m, const void* ptr, uint64_t inner,
                               uint64_t outer, uint32_t box_rows);
 // SMs of the current device (cached per device).
 int device_sm_count();
+// Whether a pointer lies on a multiple of a (a power of two).
+inline bool aligned(const void* p, unsigned a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
 
 // ---------------------------------------------------------------- device
 #ifdef __CUDACC__
@@ -240,6 +244,15 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
+}
+
+// Two fp32 products at once, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
