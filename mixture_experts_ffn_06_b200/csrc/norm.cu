@@ -10,8 +10,8 @@
 // Bound: HBM.  A row is read once and kept in registers (8 bf16 values per
 // 16-byte vector, VPT vectors per thread) through its up to three reductions,
 // so every input byte is read once and every output byte written once.  B200:
-// T = 8192, H = 2816, both norms 35.9 us (5.1 TB/s, 78 % of the measured copy bandwidth);
-// T = 16383, H = 2048, with codes 61.9 us (4.9 TB/s; the instructions of the rounding to
+// T = 8192, H = 2816, both norms 35.3 us (5.2 TB/s, 80 % of the measured copy bandwidth);
+// T = 16383, H = 2048, with codes 61.5 us (4.9 TB/s; the instructions of the rounding to
 // codes come next, issued in 68 % of the cycles); T = 1 2.7 us.
 //
 // The means are taken in double (a square of a bf16 value is exact in fp32),
@@ -164,7 +164,11 @@ __device__ __forceinline__ uint2 codes8(const float2 (&f)[4], float s, float inv
   return o;
 }
 
-template <int VPT>
+// AFTER: with the norm after a block and the residual; BEFORE: with the norm ahead of the
+// next; neither: the quantiser alone.  (One kernel that branches on what it is given keeps
+// more registers and fewer rows on an SM: T = 148, H = 2048 with codes 3.66 us and here
+// 3.39; the quantiser at 8192 x 2816 18.8 and 17.7, 3.9 TB/s.)
+template <int VPT, bool AFTER, bool BEFORE>
 __global__ void __launch_bounds__(1024)
 rows_kernel(const RowParams p) {
   __shared__ double red[2][32];
@@ -179,7 +183,7 @@ rows_kernel(const RowParams p) {
   uint4 r[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) r[j] = tid + j * nt < p.vec ? p.r[base + tid + j * nt] : zero;
-  if (p.y) {
+  if constexpr (AFTER) {
     uint4 y[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) y[j] = tid + j * nt < p.vec ? p.y[base + tid + j * nt] : zero;
@@ -211,7 +215,7 @@ rows_kernel(const RowParams p) {
       }
     }
   }
-  if (p.pre_w) {
+  if constexpr (BEFORE) {
     const float inv = rms_inverse(block_squares<VPT>(r, red[1]), p, p.pre_eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -247,6 +251,14 @@ rows_kernel(const RowParams p) {
   }
 }
 
+template <bool AFTER, bool BEFORE>
+auto pick(int vpt) {
+  return vpt == 1   ? rows_kernel<1, AFTER, BEFORE>
+         : vpt == 2 ? rows_kernel<2, AFTER, BEFORE>
+         : vpt == 3 ? rows_kernel<3, AFTER, BEFORE>
+                    : rows_kernel<4, AFTER, BEFORE>;
+}
+
 cudaError_t launch_rows(int64_t rows, RowParams& p, cudaStream_t st) {
   p.rows = rows;
   // Few rows: a thread per vector.  Many: three or four vectors per thread, which
@@ -263,10 +275,10 @@ cudaError_t launch_rows(int64_t rows, RowParams& p, cudaStream_t st) {
     if (p.vec <= 128) nt = 32, per = 8;
   }
   const int vpt = (p.vec + nt - 1) / nt;
-  auto kern = vpt == 1   ? rows_kernel<1>
-              : vpt == 2 ? rows_kernel<2>
-              : vpt == 3 ? rows_kernel<3>
-                         : rows_kernel<4>;
+  auto kern = p.y && p.pre_w ? pick<true, true>(vpt)
+              : p.y          ? pick<true, false>(vpt)
+              : p.pre_w      ? pick<false, true>(vpt)
+                             : pick<false, false>(vpt);
   return launch_ex(kern, dim3((unsigned)((rows + per - 1) / per)), dim3(nt, per), 0, st, true, p);
 }
 
