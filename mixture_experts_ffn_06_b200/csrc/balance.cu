@@ -10,7 +10,7 @@
 // that bound; the few tokens where one is not are chosen again on fp64 values
 // (exact_choice).  The weights of the k chosen are fp64 throughout.
 //
-// LT lanes take a token (8 where there are many tokens, a whole warp where there
+// LT lanes take a token (8 or 16 where there are many tokens, a whole warp where there
 // are few), each lane PER experts of one group: it sorts its values, packed with
 // their place in the low bits, by a network, so that a round of the top-k is a
 // maximum over the LT heads, and a group of one lane has its two largest in
@@ -315,7 +315,9 @@ struct Deal {
 
 constexpr int kRouteWarps = 8;
 
-template <int LT, int PER, bool K8>  // K8: k <= 8
+// TOP8: a lane keeps its eight largest alone, sorted by a shorter network; a token that
+// wants more of a lane is chosen on fp64 values (sure to be rare while k is not above LT).
+template <int LT, int PER, bool TOP8>
 __global__ void __launch_bounds__(32 * kRouteWarps, PER <= 8 ? 4 : PER <= 16 ? 3 : 2)
 balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
                const float* __restrict__ scale, int64_t T, int E, int k,
@@ -323,8 +325,8 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
                const BalanceOpt o, const Deal d) {
   constexpr int TW = 32 / LT;                // tokens per warp
   constexpr uint32_t LOW = PER - 1;          // place of an expert in its lane, reversed
-  constexpr int M = K8 && PER > 8 ? 8 : PER;  // sorted entries a lane keeps
-  constexpr int LIST = K8 ? 16 : 32;         // candidates of a token, at most
+  constexpr int M = TOP8 && PER > 8 ? 8 : PER;  // sorted entries a lane keeps
+  constexpr int LIST = LT == 8 ? 16 : 32;       // candidates of a token, at most
   extern __shared__ unsigned long long keys_s[];  // [warps][E], exact_choice's
   __shared__ int hist[kMaxExperts];
   __shared__ int16_t list_s[kRouteWarps][TW][LIST];
@@ -442,7 +444,7 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
 #pragma unroll
       for (int i = 0; i < PER; ++i) pack(i, bias && i < nv ? __ldg(bias + e0 + i * step) : 0.f);
     }
-    if constexpr (K8)
+    if constexpr (TOP8)
       top8<PER>(a);
     else
       sort<PER, 0, PER>(a);
@@ -587,17 +589,17 @@ __global__ void zero_load_kernel(int32_t* load, int E) {
   for (int e = threadIdx.x; e < E; e += blockDim.x) load[e] = 0;
 }
 
-template <int LT, bool K8>
+template <int LT, bool TOP8>
 cudaError_t launch_balance(int per, unsigned blocks, unsigned threads, const float* logits,
                            const float* bias, const float* scale, int64_t T, int E, int k,
                            int32_t* ids, float* w, int32_t* load, const BalanceOpt& o,
                            const Deal& d, cudaStream_t st) {
-  auto kern = per <= 1    ? balance_kernel<LT, 1, K8>
-              : per <= 2  ? balance_kernel<LT, 2, K8>
-              : per <= 4  ? balance_kernel<LT, 4, K8>
-              : per <= 8  ? balance_kernel<LT, 8, K8>
-              : per <= 16 ? balance_kernel<LT, 16, K8>
-                          : balance_kernel<LT, 32, K8>;
+  auto kern = per <= 1    ? balance_kernel<LT, 1, TOP8>
+              : per <= 2  ? balance_kernel<LT, 2, TOP8>
+              : per <= 4  ? balance_kernel<LT, 4, TOP8>
+              : per <= 8  ? balance_kernel<LT, 8, TOP8>
+              : per <= 16 ? balance_kernel<LT, 16, TOP8>
+                          : balance_kernel<LT, 32, TOP8>;
   const size_t smem = sizeof(unsigned long long) * (threads / 32) * E;  // at most 32 KB
   return launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, logits, bias, scale, T, E, k,
                    ids, w, load, o, d);
@@ -657,11 +659,13 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
   const bool vec = aligned(logits, 16) && aligned(bias, 16);
   // A warp per token while that leaves the SMs room; else the fewest lanes that the
   // groups and 32 experts a lane allow (E = 64, device time with 32 lanes and with 8:
-  // T = 1300 4.6 and 6.1 us, T = 4095 6.9 and 6.8, T = 8192 10.6 and 8.3).
+  // T = 1300 4.6 and 6.1 us, T = 4095 6.9 and 6.8, T = 8192 10.6 and 8.3; E = 512, k = 16,
+  // with 32 lanes and with 16: T = 4095 16.8 and 13.4, T = 16384 46.5 and 41.1).  A lane of a
+  // token writes one choice, so k lanes at least.
   int LT = 32;
   Deal d = deal(E, o.n_group, 32, vec);
-  if (k <= 8 && T > 24 * device_sm_count()) {
-    for (int lt = 8; lt < 32; lt *= 2) {
+  if (T > 24 * device_sm_count()) {
+    for (int lt = k <= 8 ? 8 : 16; lt < 32 && k <= lt; lt *= 2) {
       const Deal c = deal(E, o.n_group, lt, vec);
       if (c.n > 32) continue;
       LT = lt;

@@ -97,6 +97,12 @@ MANY = [
     (3700, 510, 8, 1, 17, 9, 2, True, 1.0),
     (3700, 128, 12, 0, 1, 1, 1, True, 1.0),
     (20000, 32, 4, 1, 1, 1, 1, True, 1.0),
+    # 16 lanes to a token for up to 16 experts, a warp for more
+    (3700, 24, 16, 0, 1, 1, 1, True, 1.0),
+    (3701, 256, 16, 1, 8, 4, 2, True, 2.5),
+    (3700, 510, 9, 1, 1, 1, 1, False, 1.0),
+    (3700, 512, 16, 0, 4, 2, 2, True, 1.0),
+    (3700, 64, 17, 1, 1, 1, 1, True, 1.0),
 ]
 
 
@@ -108,11 +114,12 @@ def test_many_tokens(api, case):
 @pytest.mark.parametrize("T", [40, 3700])
 @pytest.mark.parametrize("scoring", [0, 1])
 @pytest.mark.parametrize("spread", [0.0, 1e-7, 1e-3])
-def test_the_largest_together(api, T, scoring, spread):
+@pytest.mark.parametrize("k", [8, 15])
+def test_the_largest_together(api, T, scoring, spread, k):
     # the largest logits on the experts that one lane holds, apart by nothing, by less
     # than fp32 tells and by more; and more near equals than a candidate list takes
     g = np.random.default_rng(11)
-    E, k = 256, 8
+    E = 256
     z = g.standard_normal((T, E)).astype(np.float32)
     one_lane = [q * 32 + i for q in range(8) for i in range(4)]
     for t in range(T):
