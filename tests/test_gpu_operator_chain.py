@@ -10,6 +10,10 @@ half of a decoder layer with an INT8 dense MLP and routed experts uses them:
 Each step is held to its definition on the inputs it was given (to the bit where the
 definition fixes it; the experts' sum within 2e-2 of its RMS, the layer's bar), and
 the captured chain to the eager one."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -144,3 +148,49 @@ def test_feed_forward_half_of_a_layer(api, T):
     graph.replay()
     c.outputs()
     c.check()
+
+
+FIRST_CALLS = """
+import torch
+from mixture_experts_ffn_06_b200 import api
+g = torch.Generator(device="cuda").manual_seed(1)
+T, H, N, E, k = 64, 2048, 512, 64, 6
+r = torch.randn(T, H, device="cuda", generator=g).bfloat16()
+one = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+w = torch.randint(-128, 128, (N, H), dtype=torch.int8, device="cuda", generator=g)
+w_s = torch.rand(N, device="cuda", generator=g)
+z = torch.randn(T, E, device="cuda", generator=g)
+shape = api.make_shape(T=T, H=H, E=E, k=k, I=8)
+ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+
+def buffers():
+    return (torch.zeros(T, H, dtype=torch.int8, device="cuda"), torch.zeros(T, device="cuda"),
+            torch.zeros(T, N, dtype=torch.bfloat16, device="cuda"),
+            torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda"),
+            torch.zeros(E, dtype=torch.int32, device="cuda"))
+
+
+def run(b):
+    api.moe_block_norm(r, pre_w=one, codes=b[0], scales=b[1])
+    api.moe_quantize_rows_i8(r, b[0], b[1])
+    api.moe_linear_i8(b[0], b[1], w, w_s, b[2], ws)
+    api.moe_route_balanced(shape, z, None, None, b[3], b[4], load=b[5])
+
+
+captured, eager = buffers(), buffers()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run(captured)
+graph.replay()
+run(eager)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+assert int(captured[5].sum()) == T * k and api.moe_read_error(ws) == 0
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, check=True, timeout=300)
