@@ -18,11 +18,11 @@
 // then by the k rounds; the bytes (4 E + 8 k per token) would take a fifteenth of
 // the time.  B200, device time: T = 16384, E = 64, k = 6 10.3 us (484 GB/s; 5.7 million warp
 // instructions, issued in 54 % of the cycles); T = 4095, E = 256, k = 8 in 8 groups
-// 10.6 us; T = 64, E = 128 4.5 us; T = 1, E = 256 in groups 5.1 us.
+// 10.6 us; T = 64, E = 128 4.6 us; T = 1, E = 256 in groups 5.1 us.
 #include <cfloat>
 #include <cmath>
 
-#include "internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PER <= 8 ? 4 : PER <= 16 ? 3
 balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
                const float* __restrict__ scale, int64_t T, int E, int k,
                int32_t* __restrict__ ids, float* __restrict__ w, int32_t* __restrict__ load,
-               const BalanceOpt o, const Deal d) {
+               const BalanceOpt o, const Deal d, const bool clustered) {
   constexpr int TW = 32 / LT;                // tokens per warp
   constexpr uint32_t LOW = PER - 1;          // place of an expert in its lane, reversed
   constexpr int M = TOP8 && PER > 8 ? 8 : PER;  // sorted entries a lane keeps
@@ -574,6 +574,18 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
   }
   if (load) {
     __syncthreads();
+    if (clustered) {  // the blocks are one cluster: each sums a part of the counts over all
+      cluster_sync();
+      const uint32_t rank = cluster_ctarank(), counts = smem_u32(hist);
+      for (int e = rank * blockDim.x + threadIdx.x; e < E; e += gridDim.x * blockDim.x) {
+        int sum = 0;
+        for (uint32_t r = 0; r < gridDim.x; ++r)
+          sum += ld_cluster_s32(mapa_shared(counts + 4 * e, r));
+        load[e] = sum;
+      }
+      cluster_sync();  // no block leaves while its counts are read
+      return;
+    }
     // alone, a block writes the counts; several add theirs to zeros
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
       if (gridDim.x == 1) load[e] = hist[e];
@@ -593,7 +605,7 @@ template <int LT, bool TOP8>
 cudaError_t launch_balance(int per, unsigned blocks, unsigned threads, const float* logits,
                            const float* bias, const float* scale, int64_t T, int E, int k,
                            int32_t* ids, float* w, int32_t* load, const BalanceOpt& o,
-                           const Deal& d, cudaStream_t st) {
+                           const Deal& d, bool clustered, cudaStream_t st) {
   auto kern = per <= 1    ? balance_kernel<LT, 1, TOP8>
               : per <= 2  ? balance_kernel<LT, 2, TOP8>
               : per <= 4  ? balance_kernel<LT, 4, TOP8>
@@ -601,8 +613,22 @@ cudaError_t launch_balance(int per, unsigned blocks, unsigned threads, const flo
               : per <= 16 ? balance_kernel<LT, 16, TOP8>
                           : balance_kernel<LT, 32, TOP8>;
   const size_t smem = sizeof(unsigned long long) * (threads / 32) * E;  // at most 32 KB
-  return launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, logits, bias, scale, T, E, k,
-                   ids, w, load, o, d);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = blocks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = clustered ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, logits, bias, scale, T, E, k, ids, w, load, o, d,
+                            clustered);
 }
 
 // Deals E experts in groups to LT lanes; n > 32 where they do not fit.
@@ -678,19 +704,23 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
   const int warps = need < kRouteWarps ? (need > 0 ? (int)need : 1) : kRouteWarps;
   const int64_t all = (need + warps - 1) / warps, most = 8 * device_sm_count();
   const unsigned blocks = (unsigned)(all < most ? all : most);
-  if (load && blocks != 1 &&
+  // Counts of several blocks: up to eight are one cluster and sum them there, more
+  // add them to zeros that a launch of its own wrote (T = 64, E = 128: a call 10.2 us with
+  // two launches, 7.4 with one; replayed in a graph 4.4 and 4.6).
+  const bool clustered = load && blocks > 1 && blocks <= 8;
+  if (load && blocks != 1 && !clustered &&
       launch_ex(zero_load_kernel, dim3(1), dim3(256), 0, stream, true, load, E) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (T == 0) return MOE_OK;
   const unsigned threads = 32 * warps;
   const cudaError_t e =
       LT == 8    ? launch_balance<8, true>(d.n, blocks, threads, logits, bias, scale, T, E, k, ids,
-                                           w, load, o, d, stream)
+                                           w, load, o, d, clustered, stream)
       : LT == 16 ? launch_balance<16, true>(d.n, blocks, threads, logits, bias, scale, T, E, k,
-                                            ids, w, load, o, d, stream)
+                                            ids, w, load, o, d, clustered, stream)
       : k <= 8   ? launch_balance<32, true>(d.n, blocks, threads, logits, bias, scale, T, E, k,
-                                            ids, w, load, o, d, stream)
+                                            ids, w, load, o, d, clustered, stream)
                  : launch_balance<32, false>(d.n, blocks, threads, logits, bias, scale, T, E, k,
-                                             ids, w, load, o, d, stream);
+                                             ids, w, load, o, d, clustered, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -101,12 +101,6 @@ __device__ __forceinline__ float lin_act(float g) {
   return __fdividef(g, 1.0f + __expf(e));
 }
 
-__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
-  int32_t v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-
 // 16 bytes of a weight row, which pass through once
 __device__ __forceinline__ int4 ld_stream(const int4* p) {
   int4 v;

@@ -242,6 +242,13 @@ def test_the_bias_moves_the_choice_and_never_the_weight(api):
     assert np.allclose(w.cpu().numpy(), s / s.sum(), rtol=RTOL, atol=0)
 
 
+@pytest.mark.parametrize("T", [8, 9, 17, 25, 33, 41, 49, 57, 64, 65])
+def test_the_load_of_one_to_nine_blocks(api, T):
+    z = np.random.default_rng(T).standard_normal((T, 300)).astype(np.float32)
+    for _ in range(3):
+        _check(_run(api, z, 8), ref.route(z, 8))
+
+
 def test_an_empty_batch_clears_the_load(api):
     load = torch.full((16,), 9, dtype=torch.int32, device="cuda")
     e = torch.empty(0, device="cuda")
