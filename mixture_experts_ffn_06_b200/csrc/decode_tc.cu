@@ -214,11 +214,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmA,
   }
   // the routing (meta, slots) and, for w2, h come from the kernels before
   pdl_wait();
-  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  pdl_trigger();  // not before the block owns its columns (pdl_trigger's comment)
   const DtRange rg = dt_range(__ldg(p.meta), p.RB, p.KB);
   const int total = rg.total, Cn = rg.Cn, s0 = rg.s0, s1 = rg.s1;
 

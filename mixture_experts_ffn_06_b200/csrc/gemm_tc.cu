@@ -246,7 +246,6 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   // everything above overlaps the previous kernel when launched with PDL;
   // the expert offsets and the operands are its outputs
   pdl_wait();
-  pdl_trigger();
   for (int i = threadIdx.x; i <= p.G; i += THREADS) offs[i] = p.offsets[i];
   __syncthreads();
   if (warp == 0) {
@@ -277,6 +276,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
   if (CG == 2) cluster_sync();  // the peer's barriers are initialised
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  pdl_trigger();  // not before the block owns its columns (pdl_trigger's comment)
   const int64_t total = ub[p.G];
 
   if (warp == 0) {

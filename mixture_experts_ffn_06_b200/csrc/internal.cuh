@@ -267,7 +267,10 @@ __device__ __forceinline__ void record_error(uint32_t* err, uint32_t code) {
 // may start while its predecessor on the stream is still running; it must
 // call pdl_wait() before touching anything the predecessor writes (the wait
 // returns at once when there is no such predecessor).  pdl_trigger() lets the
-// next kernel start launching.
+// next kernel start launching, once every block has called it or ended.  A kernel with
+// TMEM calls it behind the barrier that publishes its columns: tcgen05.alloc waits without
+// a limit, and blocks of the next kernel that took the columns first would keep them in
+// their pdl_wait() for good.
 __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

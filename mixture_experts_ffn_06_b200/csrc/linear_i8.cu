@@ -292,12 +292,12 @@ linear_i8_kernel(const __grid_constant__ CUtensorMap tmW,
       tmem_alloc(smem_u32(&ctl->tmem_base), p.cols);
   }
   pdl_wait();
-  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();  // the peer's barriers are initialised
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  pdl_trigger();  // not before the block owns its columns (pdl_trigger's comment)
 
   // (fewer than 2^31 tiles: the host checks)
   const uint32_t total = (uint32_t)p.MT * p.TT;
