@@ -37,6 +37,7 @@
 #include <algorithm>
 
 #include "tc_ptx.cuh"
+#include "tmem_share.cuh"
 
 namespace moe {
 namespace {
@@ -549,6 +550,7 @@ cudaError_t launch_dt(const DecodeArgs& a, const void* b_ptr, void* out,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(smem >= tmem_smem_least(DtCfg<N>::TMEM_COLS), "and columns for all on it");
   e = cudaFuncSetAttribute(decode_tc_kernel<N, MODE, F8>,
                            cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared);

@@ -34,6 +34,7 @@
 #include <mutex>
 
 #include "tc_ptx.cuh"
+#include "tmem_share.cuh"
 
 namespace moe {
 namespace {
@@ -741,6 +742,9 @@ cudaError_t launch_mode(const GroupedGemmArgs& a, cudaStream_t st, bool pdl) {
   p.b_scale = a.b_scale;
   p.b_scale_sh = a.b_scale_sh;
 
+  static_assert(1024 + (size_t)C::STAGES * (A_STAGE + C::B_STAGE) + sizeof(EpiSmem<F8>) +
+                        sizeof(Ctl) >= tmem_smem_least(TMEM_COLS),
+                "no other block with TMEM fits beside this one");
   const size_t smem = 1024 + (size_t)C::STAGES * (A_STAGE + C::B_STAGE) +
                       sizeof(EpiSmem<F8>) + sizeof(Ctl) +
                       (sizeof(int64_t) + sizeof(int32_t)) * (size_t)(a.G + 1);

@@ -10,7 +10,7 @@
 // each epilogue warp, 16 gate rows and then the matching 16 up rows (one 3D
 // TMA box over w [2, I, K]), so lane l's partner is lane l + 16.
 //
-// Which form runs depends on what bounds it (run_linear at the end has the rules):
+// Which form runs depends on what bounds it (linear_plan.cuh has the rules):
 //   few tokens, streaming w: small independent blocks with mma.sync
 //               (linear_i8_few_kernel; gated 4096 x 28672, T = 1: 20.2 us, 5.8 TB/s, 88 % of
 //               the measured copy bandwidth);
@@ -33,16 +33,13 @@
 #include <atomic>
 #include <mutex>
 
+#include "linear_plan.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kABytes = 128 * 128;   // 128 weight rows x 128 bytes of K
-constexpr int kMaxStages = 12;
 constexpr uint64_t kTimeoutNs = 1000000000ull;  // 1 s per wait
-constexpr int kSmemMax = 227 * 1024;
-constexpr int kScaleBytes = 4096;  // token scales of the epilogue warps, at most
 constexpr int kMaxDev = 64;
 
 struct LinParams {
@@ -73,6 +70,7 @@ struct LinCtl {
   uint32_t tmem_base;
   int32_t abort_flag;
 };
+static_assert(sizeof(LinCtl) + 4096 <= kLinStatic, "with the token scales of sixteen warps");
 
 // mbar_wait, with the first tries made here: the timed wait reads the global
 // timer, which costs as much as several k-blocks.
@@ -721,8 +719,6 @@ cudaError_t make_gated_map(CUtensorMap* m, const void* ptr, uint64_t K, uint64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
 // The shared-memory opt-in of a kernel, once per device.
 template <int CG, bool GATED, int SPLIT, int EW>
 cudaError_t set_smem(int dev) {
@@ -730,14 +726,14 @@ cudaError_t set_smem(int dev) {
   if (dev >= 0 && dev < kMaxDev && ready[dev].load()) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(linear_i8_kernel<CG, GATED, SPLIT, EW>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemMax - (int)sizeof(LinCtl) - kScaleBytes);
+                                             kSmemMax - kLinStatic);
   if (e == cudaSuccess && dev >= 0 && dev < kMaxDev) ready[dev].store(true);
   return e;
 }
 
 template <int CG, bool GATED, int SPLIT, int EW>
 cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, int K,
-                          int clusters, cudaStream_t st) {
+                          const LinPlan& pl, cudaStream_t st) {
   auto kern = linear_i8_kernel<CG, GATED, SPLIT, EW>;
   CUtensorMap mw, mx;
   cudaError_t e = GATED ? make_gated_map(&mw, w, K, p.NO) : make_tma_map_e4m3(&mw, w, K, p.N, 128);
@@ -748,12 +744,9 @@ cudaError_t launch_linear(const LinParams& p, const int8_t* x, const int8_t* w, 
   if ((e = set_smem<CG, GATED, SPLIT, EW>(dev)) != cudaSuccess) return e;
   constexpr int per = CG * SPLIT;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * per));
+  cfg.gridDim = dim3((unsigned)(pl.blocks * per));
   cfg.blockDim = dim3(64 + 32 * EW);
-  const size_t ring = (size_t)p.stages * (kABytes + (size_t)p.tn / CG * 128 * p.nsub);
-  // one 512-byte row of partial sums per column, read in groups of up to 32
-  const size_t part = SPLIT > 1 ? (size_t)ceil_div(p.tn, 32) * 32 * 512 : 0;
-  cfg.dynamicSmemBytes = 1024 + std::max(ring, part);
+  cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -772,43 +765,6 @@ cudaError_t launch_few(const LinParams& p, int blocks, const int8_t* x, const in
                        cudaStream_t st) {
   return launch_ex(linear_i8_few_kernel<NB, GATED, W>, dim3(blocks), dim3(32 * W), 0, st, true,
                    reinterpret_cast<const int4*>(x), reinterpret_cast<const int4*>(w), K / 16, p);
-}
-
-// The tile of the many-token form: the one with the least estimated time, from what
-// was measured on B200 for c token columns (c = 64 to 512) in ns.  A k-block takes an
-// SM of a pair max(200 + 0.27 c, 90 + 0.86 c) (217 at 64, 255 at 192, 310 at 256) and a
-// single CTA max(245 + 0.2 c, 135 + 0.86 c) (258, 300, 355), which loads all of a
-// token tile where each CTA of a pair loads half; a pair takes 900 more to start.  A
-// tile's epilogue takes about 1000 + 7 c beside the next tile's MMAs, while two
-// accumulators fit (c <= 256), and 1500 + 10 c after its own.  T = 512, K = 4096,
-// N = 14336: pairs of 256 columns 26.7 us,
-// singles 29.9, pairs of 2 x 256 30.4; T = 512, K = 2816, 2 x 2112 gated: singles of 128
-// 10.7, pairs 10.9, pairs of 256 13.9.
-struct LinPlan {
-  int cg, tn, nsub, TT;
-  double ns;
-};
-
-LinPlan plan_tiles(int64_t T, int mt128, int KB, int sms) {
-  LinPlan best{1, 0, 0, 0, 0.0};
-  for (int cg = 1; cg <= 2; ++cg)
-    for (int nsub = 1; nsub <= 2; ++nsub) {
-      const int tt0 = ceil_div(T, 256 * nsub);
-      for (int tt = tt0; tt <= tt0 + 4; ++tt) {
-        const int tn = 16 * cg * ceil_div(ceil_div(T, (int64_t)tt * nsub), 16 * cg);
-        const int TT = ceil_div(T, (int64_t)tn * nsub);
-        const int64_t rounds = (ceil_div(mt128, cg) * (int64_t)TT + sms / cg - 1) / (sms / cg);
-        const double c = (double)tn * nsub;
-        const double body = KB * (cg == 1 ? std::max(245.0 + 0.2 * c, 135.0 + 0.86 * c)
-                                          : std::max(200.0 + 0.27 * c, 90.0 + 0.86 * c));
-        const double epi = nsub == 1 ? 1000.0 + 7.0 * c : 1500.0 + 10.0 * c;
-        const double ns = (cg == 2 ? 900.0 : 0.0) +
-                          (nsub == 1 ? (rounds - 1) * std::max(body, epi) + body + epi
-                                     : rounds * (body + epi));
-        if (best.tn == 0 || ns < best.ns) best = LinPlan{cg, tn, nsub, TT, ns};
-      }
-    }
-  return best;
 }
 
 // Clusters of SPLIT CTAs that run at once on the current device, a CTA to an SM.
@@ -841,78 +797,29 @@ int clusters_at_once() {
 
 template <bool GATED>
 cudaError_t run_linear(LinParams p, const int8_t* x, const int8_t* w, int K, cudaStream_t st) {
-  const int sms = device_sm_count();
-  const int rows = GATED ? 64 : 128;  // output channels of 128 weight rows
-  // The small blocks, each of which walks all of K: while K is short, with sixteen warps
-  // where at most two blocks come to an SM, which keeps enough loads in flight, else with
-  // eight while the blocks are few, or read weights in two places (gated).  In us with
-  // sixteen, with eight and on the tcgen05 forms, T = 1: gated 2816 x 4224 4.1, 6.1, 6.1;
-  // 4096 x 4096 5.8, 7.4, 6.9; 2048 x 8192 6.5, 5.6, 6.7; 3584 x 10000 12.4, 8.6, 10.1;
-  // 4096 x 14336 16.7, 15.2, 12.9; gated 4096 x 14336 15.4, 12.1, 13.6; gated 4096 x 28672
-  // 26.0, 20.2, 21.1; 8192 x 1024 7.2, 12.2, 5.9; gated 8192 x 28672 45.7, 41.4, 38.3.  A
-  // second tile of tokens pays for small weights alone, since every block reads all
-  // tokens (T = 16, sixteen and tcgen05: gated 2816 x 4224 5.8 and 6.1, 2112 x 2816 4.2
-  // and 5.3, 4096 x 14336 20.1 and 12.9).
-  const int blocks = ceil_div(p.NO, GATED ? 8 : 16);
-  if (K <= 4096 && blocks <= 2 * sms && p.T <= 16)
-    return p.T <= 8 ? launch_few<1, GATED, 16>(p, blocks, x, w, K, st)
-                    : launch_few<2, GATED, 16>(p, blocks, x, w, K, st);
-  if (K <= 4096 && (GATED || blocks <= 5 * sms) && p.T <= 8)
-    return launch_few<1, GATED, 8>(p, blocks, x, w, K, st);
-  p.KB = ceil_div(K, 128);
-  const int mt128 = ceil_div(p.NO, rows);
-  // Tiles of 128 weight rows and up to 128 tokens, K split as far as the clusters all
-  // run at once, a CTA to an SM (on B200 15 clusters of eight, 33 of four, 74 of two:
-  // not all SMs are in full clusters).  K = 8192, T = 64, in us with 1, 2, 4 and 8 CTAs:
-  // 14 tiles 19.1, 12.3, 8.5, 7.4; 16 tiles 19.1, 12.2, 8.6, 13.8; 36 tiles 19.3, 12.6,
-  // 18.0, 17.0; 80 tiles 20.2, 18.6, 29.8.  Handing the sums over costs as much as 5 k-blocks
-  // and one more for every 18 columns (4 tiles, T = 128, split and not: K = 1024 5.5
-  // and 4.6, K = 2048 5.7 and 6.4, K = 8192 7.2 and 16.7).
-  const int TT = ceil_div(p.T, 128), tn = 16 * ceil_div(ceil_div(p.T, TT), 16);
-  const int64_t small = (int64_t)mt128 * TT;
-  int split = 1;
-  if (small <= sms / 2) {
-    split = small <= clusters_at_once<8>() ? 8 : small <= clusters_at_once<4>() ? 4 : 2;
-    while (split > p.KB) split /= 2;
-    if (p.KB * (split - 1.0) / split <= 5.0 + tn / 18.0) split = 1;
-  }
-  // Unsplit tiles with several CTAs to an SM where there are more of them than SMs
-  // (T = 64, K = 2816: 150 tiles 12.4 us, on persistent CTAs 16.6; 300 tiles 22.1 and 24.3),
-  // and for the fewest tokens, whose short epilogue needs no sixteen warps (T = 17,
-  // K = 2816, 100 tiles: 9.4 and 10.2; T = 64: 10.1 and 9.9; T = 128: 12.0 and 10.4).
-  if (split > 1 || (p.T <= 128 && (mt128 > sms || p.T <= 32))) {
-    p.nsub = 1;
-    p.tn = tn;
-    p.nbuf = 1;
-    p.TT = ceil_div(p.T, tn);
-    p.panel = 1;
-    p.MT = mt128;
-    p.cols = p.tn <= 32 ? 32 : p.tn <= 64 ? 64 : 128;
-    // without a split, all CTAs resident at once where two or three fit an SM
-    const int res = split > 1 ? 1 : std::min(3, ceil_div(mt128, sms));
-    const int stage = kABytes + tn * 128;
-    p.stages = std::min({kMaxStages, (kSmemMax / res - 4 * 1024) / stage, ceil_div(p.KB, split)});
-    const int tiles = (int)p.MT * p.TT;
-    if (split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, tiles, st);
-    if (split == 2) return launch_linear<1, GATED, 2, 8>(p, x, w, K, tiles, st);
-    if (split == 4) return launch_linear<1, GATED, 4, 8>(p, x, w, K, tiles, st);
-    return launch_linear<1, GATED, 8, 8>(p, x, w, K, tiles, st);
-  }
-  const LinPlan pl = plan_tiles(p.T, mt128, p.KB, sms);
+  const LinPlan pl = plan_linear(p.T, p.NO, K, GATED, device_sm_count(), [](int split) {
+    return split == 8 ? clusters_at_once<8>() : clusters_at_once<4>();
+  });
+  if (pl.few == 16)
+    return p.T <= 8 ? launch_few<1, GATED, 16>(p, pl.blocks, x, w, K, st)
+                    : launch_few<2, GATED, 16>(p, pl.blocks, x, w, K, st);
+  if (pl.few) return launch_few<1, GATED, 8>(p, pl.blocks, x, w, K, st);
+  if (pl.blocks == 0) return cudaErrorInvalidValue;
+  p.KB = pl.KB;
   p.tn = pl.tn;
   p.nsub = pl.nsub;
-  p.nbuf = pl.nsub == 1 ? 2 : 1;
+  p.nbuf = pl.nbuf;
+  p.stages = pl.stages;
+  p.MT = pl.MT;
   p.TT = pl.TT;
-  p.panel = 16;
-  p.MT = ceil_div(mt128, pl.cg);
-  p.cols = 512;
-  const int stage = kABytes + p.tn / pl.cg * 128 * p.nsub;
-  p.stages = std::min(kMaxStages, (kSmemMax - 6 * 1024) / stage);
-  const int64_t tiles = (int64_t)p.MT * p.TT;
-  if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  if (pl.cg == 1)
-    return launch_linear<1, GATED, 1, 16>(p, x, w, K, (int)std::min<int64_t>(sms, tiles), st);
-  return launch_linear<2, GATED, 1, 16>(p, x, w, K, (int)std::min<int64_t>(sms / 2, tiles), st);
+  p.panel = pl.panel;
+  p.cols = pl.cols;
+  if (pl.cg == 2) return launch_linear<2, GATED, 1, 16>(p, x, w, K, pl, st);
+  if (pl.ew == 16) return launch_linear<1, GATED, 1, 16>(p, x, w, K, pl, st);
+  if (pl.split == 1) return launch_linear<1, GATED, 1, 4>(p, x, w, K, pl, st);
+  if (pl.split == 2) return launch_linear<1, GATED, 2, 8>(p, x, w, K, pl, st);
+  if (pl.split == 4) return launch_linear<1, GATED, 4, 8>(p, x, w, K, pl, st);
+  return launch_linear<1, GATED, 8, 8>(p, x, w, K, pl, st);
 }
 
 }  // namespace

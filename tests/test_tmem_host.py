@@ -8,6 +8,7 @@ let them)."""
 import glob
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -42,3 +43,76 @@ def test_dependents_start_behind_the_allocation(kernel):
     barrier = body.rindex("__syncthreads()", 0, owned)  # the barrier that publishes the columns
     triggers = [m.start() for m in re.finditer(r"pdl_trigger\(\)", body)]
     assert alloc < barrier and triggers and min(triggers) > owned
+
+
+# Blocks on an SM together ask for no more columns than it has.  What a plan of the int8
+# product takes is counted here from the sizes of an SM, not from the library's own rule:
+# the system's 1 KB and the dynamic shared memory alone (static adds to it).
+SWEEP = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "linear_plan.cuh"
+using namespace moe;
+int main() {
+  const long long SM = 228 * 1024;
+  std::vector<long long> Ts, Ns, Ks;
+  for (int t = 1; t <= 130; ++t) Ts.push_back(t);
+  for (long long t : {160, 192, 255, 256, 257, 300, 511, 512, 600, 1000, 1024, 1030, 4096, 9999,
+                      16384, 1000000, (1 << 24) - 1}) Ts.push_back(t);
+  for (long long k : {16, 48, 128, 144, 256, 400, 512, 1040, 2048, 2816, 4096, 4112, 8192, 14336,
+                      131056}) Ks.push_back(k);
+  for (long long n : {1, 7, 64, 130, 500, 1000, 2816, 4096, 9000, 14336, 28672, 40000, 128256,
+                      (1 << 22) - 1}) Ns.push_back(n);
+  struct Seen { int cols; long long smem; };
+  std::vector<Seen> seen;  // per number of columns the smallest block
+  for (int sms : {148, 132})
+    for (int fit : {1, 0})
+      for (int gated : {0, 1})
+        for (long long T : Ts) for (long long N : Ns) for (long long K : Ks) {
+          const int NO = gated ? (int)(N + 1) / 2 : (int)N;
+          const LinPlan p = plan_linear(T, NO, (int)K, gated != 0, sms, [&](int s) {
+            return fit ? (s == 8 ? 15 : 33) : 0; });
+          if (p.few || p.blocks == 0) continue;
+          auto bad = [&](const char* what) {
+            printf("%s: T %lld NO %d K %lld gated %d\n", what, T, NO, K, gated); exit(1); };
+          const long long rows = gated ? 64 : 128, stage = 128 * 128 + p.tn / p.cg * 128 * p.nsub;
+          if (p.stages < 1 || p.stages > kMaxStages) bad("stages");
+          if ((long long)p.smem < 1024 + p.stages * stage) bad("ring");
+          if (p.split > 1 && (long long)p.smem < 1024 + (p.tn + 31) / 32 * 32 * 512) bad("sums");
+          if (p.smem + kLinStatic > 227 * 1024) bad("too much shared memory");
+          if (p.tn % (16 * p.cg) || p.tn < 16 || p.tn > 256) bad("columns of an MMA");
+          const int used = p.nbuf * p.nsub == 2 ? 256 + p.tn : (p.tn + 31) / 32 * 32;
+          if (used > (int)p.cols || p.nbuf * p.nsub > 2) bad("columns");
+          if (p.MT * p.cg * rows < NO || (long long)p.TT * p.nsub * p.tn < T) bad("cover");
+          if (p.split > 1 && (p.KB < p.split || p.blocks != (int)(p.MT * p.TT))) bad("split");
+          bool found = false;
+          for (Seen& s : seen)
+            if (s.cols == (int)p.cols) {
+              found = true;
+              if ((long long)p.smem + 1024 < s.smem) s.smem = p.smem + 1024;
+            }
+          if (!found) seen.push_back({(int)p.cols, (long long)p.smem + 1024});
+        }
+  // the other kernels with TMEM: expert products and decode products, their smallest
+  for (auto s : {Seen{512, 214704}, Seen{128, 92000}, Seen{64, 90000}}) seen.push_back(s);
+  // the most columns that blocks of any kinds sharing an SM ask for
+  std::vector<int> most(SM / 16 + 1, 0);
+  for (long long m = 0; m <= SM / 16; ++m)
+    for (const Seen& s : seen) {
+      const long long rest = m - (s.smem + 15) / 16;
+      if (rest >= 0 && most[rest] + s.cols > most[m]) most[m] = most[rest] + s.cols;
+    }
+  for (const Seen& s : seen) printf("%d columns: %lld bytes\n", s.cols, s.smem);
+  printf("columns asked for together: %d\n", most[SM / 16]);
+  return most[SM / 16] > 512;
+}
+"""
+
+
+def test_blocks_that_share_an_sm_share_its_columns(tmp_path):
+    src, exe = tmp_path / "sweep.cpp", tmp_path / "sweep"
+    src.write_text(SWEEP)
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-I", CSRC, "-x", "c++", "-o", str(exe), str(src)])
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout + run.stderr
