@@ -1,8 +1,15 @@
-"""Int8 products on the forms that the small sizes do not reach."""
+"""Gated int8 products into bf16 alone, on every form: neighbouring lanes swap
+channels there for 4-byte stores, where an fp32 output keeps each lane to its own.
+Both ways hold the same fp32 value, so the bf16 rows have to be equal to the bit."""
 import pytest
 import torch
 
+from linear_forms import FORMS
+
 pytestmark = pytest.mark.gpu
+
+RTOL, ATOL = 2.0 ** -13, 1e-30   # of the fp32 output, as derived in test_gpu_linear_i8.py
+BAND = 2048                      # values in front of and behind an output
 
 
 @pytest.fixture(scope="module")
@@ -19,6 +26,32 @@ def _inputs(T, N, K):
     xs = (0.5 + torch.rand(T, device="cuda", generator=g)) / 127
     ws = (0.5 + torch.rand(N, device="cuda", generator=g)) / 127 / K ** 0.5
     return x, xs, w, ws
+
+
+@pytest.mark.parametrize("T,N,K", FORMS)
+def test_bf16_alone(api, T, N, K):
+    x, xs, w, ws = _inputs(T, N, K)
+    n = N // 2
+    work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    v = (x.double() @ w.double().T).float() * (xs[:, None] * ws)
+    for act in (api.ACT_SILU, api.ACT_GELU_TANH):
+        o32 = torch.full((T, n), float("nan"), device="cuda")
+        both = torch.full((T, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+        api.moe_linear_i8(x, xs, w, ws, both, work, gate_act=act, out_f32=o32)
+        raw = torch.full((BAND + T * n + BAND,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        alone = raw[BAND:BAND + T * n].view(T, n)
+        api.moe_linear_i8(x, xs, w, ws, alone, work, gate_act=act)
+        assert api.moe_read_error(work) == 0
+        g = v[:, :n].double()
+        if act == api.ACT_GELU_TANH:
+            g = g / (1 + torch.exp(-2 * (2 / torch.pi) ** 0.5 * (g + 0.044715 * g ** 3)))
+        else:
+            g = g / (1 + torch.exp(-g))
+        want = g * v[:, n:].double()
+        assert bool(((o32 - want).abs() <= RTOL * want.abs() + ATOL).all())
+        assert torch.equal(both, o32.to(torch.bfloat16))
+        assert torch.equal(alone, both)
+        assert bool(raw[:BAND].isnan().all()) and bool(raw[BAND + T * n:].isnan().all())
 
 
 def test_short_tiles_one_launch_behind_the_other(api):

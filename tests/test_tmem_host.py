@@ -12,6 +12,8 @@ import subprocess
 
 import pytest
 
+from linear_forms import FORMS
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "mixture_experts_ffn_06_b200", "csrc")
 
@@ -116,3 +118,26 @@ def test_blocks_that_share_an_sm_share_its_columns(tmp_path):
     subprocess.check_call(["g++", "-std=c++17", "-O1", "-I", CSRC, "-x", "c++", "-o", str(exe), str(src)])
     run = subprocess.run([str(exe)], capture_output=True, text=True)
     assert run.returncode == 0, run.stdout + run.stderr
+
+
+PLAN = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "linear_plan.cuh"
+int main(int n, char** v) {
+  for (int i = 1; i + 2 < n; i += 3) {
+    const moe::LinPlan p = moe::plan_linear(atoll(v[i]), atoi(v[i + 1]) / 2, atoi(v[i + 2]), true, 148,
+                                            [](int s) { return s == 8 ? 15 : 33; });
+    printf("%d %d %d %d %d\n", p.few, p.cg, p.split, p.ew, p.nsub);
+  }
+}
+"""
+
+
+def test_the_sizes_that_stand_for_a_form_reach_it(tmp_path):
+    src, exe = tmp_path / "plan.cpp", tmp_path / "plan"
+    src.write_text(PLAN)
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-I", CSRC, "-x", "c++", "-o", str(exe), str(src)])
+    out = subprocess.check_output([str(exe), *(str(n) for size in FORMS for n in size)], text=True)
+    got = [tuple(int(n) for n in line.split()) for line in out.splitlines()]
+    assert got == [(0, *form) for form in FORMS.values()]
