@@ -469,8 +469,8 @@ MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const moe_bf16* x,
  *   w_j  = s_id, divided by the sum of the k chosen s when renorm is set
  *        (0 when that sum is 0), times factor, times scale[id]
  * Computed in fp64 and rounded once to fp32, but for the softmax's
- * denominator without renorm, whose terms are fp32 exponentials (relative
- * error below 1e-6).
+ * denominator without renorm, which is within 2^-25 of its value (so a weight is
+ * within 2^-24 + 2^-25).
  *   logits [T,E] fp32, bias [E] fp32 or NULL (zeros), scale [E] fp32 or NULL
  *   opts   NULL is {MOE_SCORE_SOFTMAX, 0, 0, 1, 1, 1.0f}
  *   ids, w [T,k] out;  load [E] int32 out or NULL: how many of the T*k

@@ -87,6 +87,54 @@ __device__ __forceinline__ float choice32(float term, float inv, float b, bool s
   return available(term) && c == c ? c : -INFINITY;
 }
 
+// A softmax's denominator as it is added up: hi + lo.
+struct Sum2 {
+  float2 hi, lo;
+};
+
+__device__ __forceinline__ float2 minus2(float2 a, float2 b) { return fma2(b, both(-1.0f), a); }
+
+// a + b as the rounded sum and its error (2Sum).
+__device__ __forceinline__ float2 two_sum(float2 a, float2 b, float2& err) {
+  const float2 s = add2(a, b), bb = minus2(s, a);
+  err = add2(minus2(a, minus2(s, bb)), minus2(b, bb));
+  return s;
+}
+
+// e^(z - m), z <= m, of two logits, added to the sum without the roundings of the
+// difference, of the exponential and of the sum.  With x + e = z - m exactly, n = rint(x / ln 2)
+// and r + rl = x + e - n ln 2, a term is 2^n (1 + r + q)(1 + rl), q the series from r^2 / 2 to
+// r^7 / 7! (the rest is below 2^-27 at |r| <= ln 2 / 2) and 1 + r split exactly.  What rounds is
+// below a tenth of a term, so the sum is within 2^-25.  Below e^-87, and for NaN, a term
+// counts as that.  (T = 16384, E = 64, k = 6 11.2 us, with terms from expf added in fp64,
+// which left weights 1.7 roundings off, 10.9; E = 512, k = 8 43.3 and 46.1.)
+__device__ __forceinline__ float2 exp_below(float2 z, float m, Sum2& sum) {
+  float2 e, x = two_sum(z, both(-m), e);
+  e.x = x.x > -87.0f ? e.x : 0.0f;
+  e.y = x.y > -87.0f ? e.y : 0.0f;
+  x = make_float2(fmaxf(x.x, -87.0f), fmaxf(x.y, -87.0f));
+  const float2 k = fma2(x, both(1.44269504f), both(12582912.0f));  // 1.5 2^23: n in the low bits
+  const float2 n = add2(k, both(-12582912.0f));
+  // ln 2 in 16 bits and what is left of it
+  const float2 r = fma2(n, both(-0.693145751953125f), x);
+  const float2 rl = fma2(n, both(-1.42860682e-06f), e);
+  float2 p = fma2(r, both(1.98412701e-04f), both(1.38888892e-03f));  // 1/7!, 1/6!
+  p = fma2(p, r, both(8.33333377e-03f));
+  p = fma2(p, r, both(4.16666679e-02f));
+  p = fma2(p, r, both(1.66666672e-01f));
+  p = fma2(p, r, both(0.5f));
+  const float2 h = add2(both(1.0f), r);
+  float2 l = add2(minus2(both(1.0f), h), r);  // 1 + r = h + l
+  const float2 q = mul2(mul2(r, r), p);
+  l = add2(l, fma2(rl, add2(h, q), q));
+  const float2 f = make_float2(__int_as_float((__float_as_int(k.x) << 23) + 0x3f800000),
+                               __int_as_float((__float_as_int(k.y) << 23) + 0x3f800000));
+  const float2 hf = mul2(h, f), lf = mul2(l, f);
+  sum.hi = two_sum(sum.hi, hf, e);
+  sum.lo = add2(sum.lo, add2(e, lf));
+  return add2(hf, lf);
+}
+
 // Puts n <= 32 candidates of a token in their order, by the whole warp: each lane
 // forms one's value and counts those before it.  In fp32 first, without the
 // packing's error; where two are still within err of each other, in fp64, equal
@@ -399,18 +447,31 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
     float inv = 1.0f;
     double den = 0.0;
     if (!sigmoid) {
-      float sum = 0.0f;
+      if (o.renorm) {  // the denominator cancels out of the weights
+        float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const bool a = available(z[i]);
-        if (!o.renorm && a) den += (double)expf(z[i] - zmax);
-        z[i] = a ? __expf(z[i] - zmax) : z[i];  // now the term, or -inf / NaN
-        sum += a ? z[i] : 0.0f;
+        for (int i = 0; i < PER; ++i) {
+          const bool a = available(z[i]);
+          z[i] = a ? __expf(z[i] - zmax) : z[i];  // now the term, or -inf / NaN
+          sum += a ? z[i] : 0.0f;
+        }
+#pragma unroll
+        for (int s = LT / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(kAll, sum, s);
+        inv = __fdividef(1.0f, sum);
+      } else {
+        Sum2 sum{both(0.0f), both(0.0f)};
+        const float m = fmaxf(zmax, -FLT_MAX);  // (-inf where no expert is available)
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+          const float z1 = i + 1 < PER ? z[i + 1] : -INFINITY;
+          const float2 term = exp_below(make_float2(z[i], z1), m, sum);
+          if (available(z[i])) z[i] = term.x;
+          if (i + 1 < PER && available(z1)) z[i + 1] = term.y;
+        }
+        den = token_sum<LT>(((double)sum.hi.x + (double)sum.hi.y) +
+                            ((double)sum.lo.x + (double)sum.lo.y));
+        inv = __fdividef(1.0f, (float)den);
       }
-#pragma unroll
-      for (int s = LT / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(kAll, sum, s);
-      if (!o.renorm) den = token_sum<LT>(den);
-      inv = __fdividef(1.0f, sum);
       err = 7.6293945e-06f * inv;  // 2^-17 of the largest score
     }
     uint32_t a[PER];

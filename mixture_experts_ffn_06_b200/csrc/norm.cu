@@ -38,16 +38,6 @@ struct RowParams {
   double n, inv_n;  // values per row, 1 / n
 };
 
-// Two fp32 sums at once, each rounded to nearest (mul2: two products).
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<const float2*>(&r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 __device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
