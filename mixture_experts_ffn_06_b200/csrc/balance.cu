@@ -438,11 +438,14 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
       zmax = fmaxf(zmax, z[i]);  // a NaN is passed over
     }
     zmax = token_max<LT>(zmax);
-    // Scores.  The fp32 exponential is within |x| 2^-23 + 2^-22 of its value and the
-    // division within 2^-22; s (1 - s) <= 1/4 and |x| s (1 - s) < 0.23 leave a sigmoid
-    // within 3.4e-7, and with |x| e^-|x| < 0.37 a softmax's term is within 2^-21 of
-    // the largest.  Its denominator adds at most ln(512) 2^-23 + 2^-22 and
-    // 21 roundings: 2^-18 of the largest score in all.
+    // Scores, and a bound on the error of a difference of two, in units of 2^-23.  __expf
+    // is within 2 + 1.173 |x|.  A sigmoid: s (1 - s) (2 + 1.173 |z|) from it, s / 2 and 2 s from
+    // the sum and the division, 2.67 at most: 5.4 for two, taken as 5.7.  A softmax's
+    // term, with the rounding of z - zmax: 2 + 1.7 |x| of e^x, which never is above 2 of
+    // the largest; half of the score for the product with inv: 5 for two.  The
+    // denominator's error is common to both and so counts once, times their difference:
+    // the mean of its terms' errors, 2 + 1.7 ln 512 = 12.7, half for each of up to 36
+    // additions in a row, 2 for the division.  38 of the largest score, taken as 64.
     float err = 6.8e-07f;  // of two values
     float inv = 1.0f;
     double den = 0.0;
@@ -472,7 +475,7 @@ balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
                             ((double)sum.lo.x + (double)sum.lo.y));
         inv = __fdividef(1.0f, (float)den);
       }
-      err = 7.6293945e-06f * inv;  // 2^-17 of the largest score
+      err = 7.6293945e-06f * inv;  // 2^-17: inv is the largest score
     }
     uint32_t a[PER];
     float v0 = -INFINITY, v1 = -INFINITY;  // this lane's two largest c (for its group)
