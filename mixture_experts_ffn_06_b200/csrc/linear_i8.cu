@@ -89,8 +89,14 @@ __device__ __forceinline__ bool wait_for_cluster(uint32_t bar, uint32_t parity,
   return mbar_wait_cluster(bar, parity, abort_flag, kTimeoutNs, err);
 }
 
-// Both activations as g sigma(.): 0.5 (1 + tanh v) = sigma(2v) does not cancel
-// where v is large and negative.
+// Both activations as g sigma(x): 0.5 (1 + tanh v) = sigma(2v) does not cancel
+// where v is large and negative.  In units of 2^-23, __expf is within 2 + 1.173 |x|, GELU's x
+// (six roundings) brings 3 |x|, the sum, the division and the product with the up value
+// 3 together: 5 + 1.2 max(-x, 0) and 5 + 4.2 max(-x, 0), as the exponential counts by sigma(-x).
+// At x = -8 that is a 400th of the rounding to bf16 (2^-9), and expf with an IEEE division,
+// which leave 3 at any x, cost too much there: gated 4096 x 28672, T = 8 24.8 us and here
+// 21.0, 1408 x 2816, T = 16384 65 and 56; an exponential with its argument's remainder
+// (4 at any x) 21.0 and 61.
 template <int ACT>
 __device__ __forceinline__ float lin_act(float g) {
   const float e = ACT == MOE_ACT_SILU

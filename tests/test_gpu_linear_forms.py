@@ -65,3 +65,22 @@ def test_short_tiles_one_launch_behind_the_other(api):
     want = ((x.double() @ w.double().T).float() * (xs[:, None] * ws)).to(torch.bfloat16)
     assert api.moe_read_error(work) == 0
     assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 2048, 256), (40, 2048, 256), (100, 2048, 2064), (700, 2048, 256)])
+def test_gated_fp32_output_within_the_stated_error(api, T, N, K):
+    # gates from a hundredth to some hundreds: sigmoid arguments far out on both sides
+    x, xs, w, ws = _inputs(T, N, K)
+    n = N // 2
+    ws[:n] *= torch.logspace(-1, 3, n, device="cuda")
+    work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    v = (x.double() @ w.double().T).float() * (xs[:, None] * ws)
+    g, u = v[:, :n].double(), v[:, n:].double()
+    for act, c in ((api.ACT_SILU, 1.2), (api.ACT_GELU_TANH, 4.2)):
+        o32 = torch.empty(T, n, device="cuda")
+        api.moe_linear_i8(x, xs, w, ws, None, work, gate_act=act, out_f32=o32)
+        e = (8 / torch.pi) ** 0.5 * (g + 0.044715 * g ** 3) if act == api.ACT_GELU_TANH else g
+        want = g / (1 + torch.exp(-e)) * u
+        assert float(e.min()) < -100 and float(e.max()) > 100
+        bound = (5 + c * (-e).clamp(0, 90)) * 2.0 ** -23 * want.abs() + (g * u).abs() * 2.0 ** -126 + 2.0 ** -149
+        assert bool(((o32 - want).abs() <= bound).all())
