@@ -554,8 +554,11 @@ MOE_API moe_status moe_linear_i8(int64_t T, int N, int K, const int8_t* x,
  * itself; without pre_w only the first half does.  RMSNorm(v) = v *
  * (1 / sqrt(mean(v^2) + eps)), the mean taken in fp64 and rounded once to fp32;
  * each product and sum above is one fp32 operation in the order written
- * (factors that are not given are left out), so a, r' and the codes are
- * reproducible bit for bit, and equal to the steps taken one by one.
+ * (factors that are not given are left out), so a, r' and the codes are those
+ * of the steps taken one by one, and the same bits in every call of the same T
+ * and H.  Another T may sum a row's squares in another order: the same bits but
+ * where the fp64 sums fall on two sides of a border between fp32 values, when
+ * the row's norm is that of the neighbouring mean.
  *   y, r   [T,H] bf16;  post_w, pre_w, gate [H] bf16;  token_gate [T] fp32
  *   r_out  [T,H] bf16 out, required with y; may be r itself
  *   a      [T,H] bf16 out or NULL;  codes [T,H] int8 and scales [T] fp32 out,

@@ -14,10 +14,12 @@
 // T = 16383, H = 2048, with codes 61.5 us (4.9 TB/s; the instructions of the rounding to
 // codes come next, issued in 68 % of the cycles); T = 1 2.7 us.
 //
-// The means are taken in double (a square of a bf16 value is exact in fp32),
-// so that they round to the same fp32 value whatever the order of the sum, and
-// with IEEE divisions and square roots the rows and their codes come out the
-// same bits as the steps taken one by one.
+// The means are taken in double (a square of a bf16 value is exact in fp32), and with IEEE
+// divisions and square roots the rows and their codes come out the same bits as the steps
+// taken one by one.  The number of threads of a row, and with it the order of its sum,
+// depends on how many rows there are: the fp64 sums then differ in their last bits, where
+// a row's exponents span more than 53 bits hold, and round to the same fp32 mean but at a
+// border (some 2^-27 of rows).
 #include <algorithm>
 #include <cmath>
 
