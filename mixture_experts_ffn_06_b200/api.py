@@ -459,9 +459,15 @@ def _within(n, most, where):
         raise MoEError(2, where)
 
 
-def _dev(t):
+def _dev(t, what):
     """The current CUDA device; a tensor elsewhere is refused by _q."""
+    if t is None:
+        _missing(what)
     return _cuda_device() if t.is_cuda else 0
+
+
+def _missing(what):
+    raise ValueError(f"{what}: expected a tensor, got None")
 
 
 def balance_opts(scoring=SCORE_SOFTMAX, n_group=1, topk_group=1, group_top=1, renorm=True,
@@ -476,7 +482,7 @@ def moe_route_balanced(shape, logits, bias, scale, ids, w, load=None, opts=None,
     int32 and w [T,k] fp32 out, ``load`` [E] int32 out or None (choices per
     expert, overwritten); ``opts`` from balance_opts()."""
     T, E, k = shape.T, shape.E, shape.k
-    f32, i32, d = torch.float32, torch.int32, _dev(logits)
+    f32, i32, d = torch.float32, torch.int32, _dev(logits, "logits")
     st = lib.moe_route_balanced(
         shape, _q(logits, f32, T * E, d, "logits"), _q(bias, f32, E, d, "bias"),
         _q(scale, f32, E, d, "scale"), opts, _q(ids, i32, T * k, d, "ids"),
@@ -489,9 +495,11 @@ def moe_route_balanced(shape, logits, bias, scale, ids, w, load=None, opts=None,
 def moe_quantize_rows_i8(src, codes, scales, stream=None):
     """Per-row dynamic int8 quantisation of bf16 rows src [R, C] into codes
     (int8 [R, C]) and scales (fp32 [R])."""
+    if src is None:
+        _missing("src")
     R, C = src.shape
     _within(C, MAX_ROW, "moe_quantize_rows_i8")
-    d = _dev(src)
+    d = _dev(src, "src")
     st = lib.moe_quantize_rows_i8(
         _q(src, torch.bfloat16, R * C, d, "src"), R, C, _q(codes, torch.int8, R * C, d, "codes"),
         _q(scales, torch.float32, R, d, "scales"),
@@ -506,13 +514,15 @@ def moe_linear_i8(x, x_scale, w, w_scale, out, ws, gate_act=None, out_f32=None, 
     ``gate_act`` None (LINEAR_PLAIN), or ACT_SILU / ACT_GELU_TANH: w holds gate rows, then up
     rows, and out is [T,N/2] = Act(gate) * up.  ``ws``: at least 256 bytes
     (uint8), zeroed once; its error word is read by moe_read_error."""
+    if x is None or w is None or ws is None:
+        _missing("x" if x is None else "w" if w is None else "ws")
     T, K = x.shape
     N = w.shape[0]
     _within(K, LINEAR_MAX_K, "moe_linear_i8")
     _within(N, LINEAR_MAX_N, "moe_linear_i8")
     if gate_act is None:
         gate_act = LINEAR_PLAIN
-    d, i8, f32 = _dev(x), torch.int8, torch.float32
+    d, i8, f32 = _dev(x, "x"), torch.int8, torch.float32
     n_out, n_ws = T * (N if gate_act == LINEAR_PLAIN else N // 2), ws.numel()
     st = lib.moe_linear_i8(
         T, N, K, _q(x, i8, T * K, d, "x"), _q(x_scale, f32, T, d, "x_scale"),
@@ -533,9 +543,11 @@ def moe_block_norm(r, y=None, post_w=None, gate=None, token_gate=None, alpha=1.0
     post_w gate); with pre_w, a = RMSNorm(r_out) pre_w and / or its int8 codes
     [T,H] and scales [T].  post_w, pre_w and gate [H] bf16, token_gate [T]
     fp32.  r_out may be r."""
+    if r is None:
+        _missing("r")
     T, H = r.shape
     _within(H, MAX_ROW, "moe_block_norm")
-    n, d, bf, f32 = T * H, _dev(r), torch.bfloat16, torch.float32
+    n, d, bf, f32 = T * H, _dev(r, "r"), torch.bfloat16, torch.float32
     prm = moe_block_norm_params(
         _q(y, bf, n, d, "y"), _q(r, bf, n, d, "r"), _q(post_w, bf, H, d, "post_w"),
         _q(gate, bf, H, d, "gate"), _q(token_gate, f32, T, d, "token_gate"),
