@@ -635,32 +635,11 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
 
 // ------------------------------------------------------------------- host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
-                                  void*, const cuuint64_t*, const cuuint64_t*,
-                                  const cuuint32_t*, const cuuint32_t*,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault,
-                                &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 // [outer, inner] row-major tensor of bf16 (box {64, box_rows}) or of e4m3
 // bytes (f8: box {128, box_rows}); rows of 128 bytes, 128-byte swizzle.
 cudaError_t make_map(CUtensorMap* m, const void* ptr, uint64_t inner,
                      uint64_t outer, uint32_t box_rows, bool f8 = false) {
-  EncodeTiledFn enc = encode_fn();
+  const EncodeTiledFn enc = encode_tiled();
   if (!enc) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {inner * (f8 ? 1 : 2)};
@@ -802,6 +781,20 @@ __global__ void wait_selftest_kernel(uint32_t* err, uint64_t timeout_ns) {
 }
 
 }  // namespace
+
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault,
+                                &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
 
 cudaError_t launch_grouped_gemm(const GroupedGemmArgs& a, cudaStream_t st, bool pdl) {
   // CTA pairs when the experts' segments are large enough that most m-blocks

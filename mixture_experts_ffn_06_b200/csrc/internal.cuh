@@ -223,6 +223,14 @@ cudaError_t launch_grouped_gemm(const GroupedGemmArgs& a, cudaStream_t st,
 cudaError_t launch_wait_selftest(uint32_t* err, uint32_t timeout_us,
                                  cudaStream_t st);
 
+// The driver's cuTensorMapEncodeTiled, null where it has none (gemm_tc.cu).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
+                                  void*, const cuuint64_t*, const cuuint64_t*,
+                                  const cuuint32_t*, const cuuint32_t*,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
 // TMA map of a row-major bf16 [outer, inner] tensor: box {64, box_rows},
 // 128-byte swizzle, out-of-range elements read as zero (gemm_tc.cu).
 cudaError_t make_tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t inner,

@@ -31,7 +31,6 @@
 // records MOE_ERR_TIMEOUT, waits for its own copies and MMAs and frees TMEM.
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "linear_plan.cuh"
 #include "tc_ptx.cuh"
@@ -689,30 +688,10 @@ linear_i8_few_kernel(const int4* __restrict__ x, const int4* __restrict__ w, int
 
 // ------------------------------------------------------------------- host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 // Map of the gated weight as [2, I, K] bytes: box {128, 16, 2}, 16 gate rows and
 // then the matching 16 up rows (rows past I read as zero).
 cudaError_t make_gated_map(CUtensorMap* m, const void* ptr, uint64_t K, uint64_t I) {
-  EncodeTiledFn enc = encode_fn();
+  const EncodeTiledFn enc = encode_tiled();
   if (!enc) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {K, I, 2};
   const cuuint64_t strides[2] = {K, K * I};
