@@ -479,8 +479,9 @@ MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const moe_bf16* x,
  * -inf, so it comes after every available expert (by id), with weight 0; in a
  * group's sum it counts as -inf, so a group with fewer than group_top
  * available experts comes after the others.  +inf counts as the largest
- * finite value.  A non-finite bias does the same to c (NaN as -inf).  The ids
- * of a token are always k different valid expert ids, whatever the row holds.
+ * finite value.  A non-finite bias does the same to c (NaN as -inf; an expert
+ * that is chosen for want of others has weight 0 then too).  The ids of a token
+ * are always k different valid expert ids, whatever the row holds.
  * Uses no workspace; shape->H, I, n_shared, act are validated and play no
  * part.  Bad options return MOE_ERR_INVALID_ARG (MOE_ERR_UNSUPPORTED for
  * n_group > MOE_MAX_GROUPS) before any launch.
@@ -508,6 +509,7 @@ MOE_API moe_status moe_route_balanced(const moe_shape* shape, const float* logit
  * even, within +-127.  Fixed by IEEE fp32 arithmetic, so reproducible bit for
  * bit.  A row that holds an infinity or a NaN gets codes 0 and a scale that is
  * not finite (NaN if it holds a NaN), so that products with it are NaN.
+ * Other cols return MOE_ERR_INVALID_ARG (MOE_ERR_UNSUPPORTED past MOE_MAX_ROW).
  */
 #define MOE_MAX_ROW 32768
 MOE_API moe_status moe_quantize_rows_i8(const moe_bf16* src, int64_t rows, int cols,
@@ -561,7 +563,7 @@ MOE_API moe_status moe_linear_i8(int64_t T, int N, int K, const int8_t* x,
  * the row's norm is that of the neighbouring mean.
  *   y, r   [T,H] bf16;  post_w, pre_w, gate [H] bf16;  token_gate [T] fp32
  *   r_out  [T,H] bf16 out, required with y; may be r itself
- *   a      [T,H] bf16 out or NULL;  codes [T,H] int8 and scales [T] fp32 out,
+ *   a      [T,H] bf16 out or NULL, may be y itself;  codes [T,H] int8 and scales [T] fp32 out,
  *          or both NULL; with pre_w at least one of a and codes is given
  * H % 8 == 0 and H <= MOE_MAX_ROW (MOE_ERR_UNSUPPORTED otherwise), T < 2^24.
  * Rows and vectors of H are 16-byte aligned (codes 8-byte).  What is not used
