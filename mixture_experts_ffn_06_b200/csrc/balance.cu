@@ -364,7 +364,7 @@ struct Deal {
 constexpr int kRouteWarps = 8;
 
 // TOP8: a lane keeps its eight largest alone, sorted by a shorter network; a token that
-// wants more of a lane is chosen on fp64 values (sure to be rare while k is not above LT).
+// wants more of a lane is chosen on fp64 values (eight_will_do: rare where it is used).
 template <int LT, int PER, bool TOP8>
 __global__ void __launch_bounds__(32 * kRouteWarps, PER <= 8 ? 4 : PER <= 16 ? 3 : 2)
 balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
@@ -713,6 +713,19 @@ Deal deal(int E, int groups, int LT, bool aligned) {
   return d;
 }
 
+// Whether a lane's eight largest will do: fewer than eight are chosen, or they come from
+// so many lanes that all eight of one are rarely wanted (C(k, 8) lanes^-7 (1 - 1 / lanes)^(k - 8)
+// of the tokens): at most one token in 475, in 5000 where a lane has more than 16, whose
+// tokens take longer to choose again.  Where one kept group was one lane's every token was
+// chosen again: E = 256, 8 groups, 1 kept, k = 8, T = 4095 40.3 us, with all entries on 32 lanes
+// 11.2; E = 512, 32 groups, 1 kept, T = 1 21.0 and 7.4.  With eight lanes in play and
+// k = 16, sixteen lanes and all entries on 32: E = 256, T = 4500 14.0 and 14.6, T = 16384 29.3
+// and 38.0; E = 512, T = 4095 14.7 and 18.6, T = 8192 36.8 and 28.3, T = 16384 53.0 and 49.9.
+bool eight_will_do(const Deal& d, const BalanceOpt& o, int k, int LT) {
+  const int lanes = d.groups > 1 ? d.lanes * o.topk_group : LT;
+  return d.n <= 8 || k < 8 || lanes >= (d.n <= 16 ? (k + 1) / 2 : k - 4);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -748,16 +761,18 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
   const int64_t T = shape->T;
   const bool vec = aligned(logits, 16) && aligned(bias, 16);
   // A warp per token while that leaves the SMs room; else the fewest lanes that the
-  // groups and 32 experts a lane allow (E = 64, device time with 32 lanes and with 8:
-  // T = 1300 4.6 and 6.1 us, T = 4095 6.9 and 6.8, T = 8192 10.6 and 8.3; E = 512, k = 16,
-  // with 32 lanes and with 16: T = 4095 16.8 and 13.4, T = 16384 46.5 and 41.1).  A lane of a
-  // token writes one choice, so k lanes at least.
+  // groups, 32 experts a lane and eight_will_do allow.  A lane of a token writes one choice, so
+  // k lanes at least.  Sigmoid, with 8, 16 and 32 lanes: E = 64, k = 8 T = 2000 6.0, 5.0 and 5.0,
+  // T = 4500 6.5, 6.4 and 7.0, T = 8192 7.2, 7.9 and 10.5; E = 256, k = 8 in 8 groups T = 2000 10.3,
+  // 7.5 and 7.4, T = 4500 10.8, 12.1 and 11.8, T = 16384 24.7, 25.4 and 30.3; with 16 and 32: E = 256,
+  // k = 16 in 8 groups T = 2000 9.6 and 9.1, T = 3600 13.9 and 14.3, T = 6000 21.4 and 19.3,
+  // T = 16384 29.3 and 38.0; E = 512, k = 16 T = 2000 11.0 and 12.8, T = 16384 40.0 and 45.7.
   int LT = 32;
   Deal d = deal(E, o.n_group, 32, vec);
   if (T > 24 * device_sm_count()) {
     for (int lt = k <= 8 ? 8 : 16; lt < 32 && k <= lt; lt *= 2) {
       const Deal c = deal(E, o.n_group, lt, vec);
-      if (c.n > 32) continue;
+      if (c.n > 32 || !eight_will_do(c, o, k, lt)) continue;
       LT = lt;
       d = c;
       break;
@@ -777,14 +792,11 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
     return MOE_ERR_CUDA;
   if (T == 0) return MOE_OK;
   const unsigned threads = 32 * warps;
-  const cudaError_t e =
-      LT == 8    ? launch_balance<8, true>(d.n, blocks, threads, logits, bias, scale, T, E, k, ids,
-                                           w, load, o, d, clustered, stream)
-      : LT == 16 ? launch_balance<16, true>(d.n, blocks, threads, logits, bias, scale, T, E, k,
-                                            ids, w, load, o, d, clustered, stream)
-      : k <= 8   ? launch_balance<32, true>(d.n, blocks, threads, logits, bias, scale, T, E, k,
-                                            ids, w, load, o, d, clustered, stream)
-                 : launch_balance<32, false>(d.n, blocks, threads, logits, bias, scale, T, E, k,
-                                             ids, w, load, o, d, clustered, stream);
+  const bool top8 = LT < 32 || (k <= 8 && eight_will_do(d, o, k, 32));
+  auto go = LT == 8 ? launch_balance<8, true> : LT == 16 ? launch_balance<16, true>
+            : top8  ? launch_balance<32, true>
+                    : launch_balance<32, false>;
+  const cudaError_t e = go(d.n, blocks, threads, logits, bias, scale, T, E, k, ids, w, load, o, d,
+                           clustered, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
