@@ -784,9 +784,15 @@ extern "C" moe_status moe_route_balanced(const moe_shape* shape, const float* lo
   const int64_t all = (need + warps - 1) / warps, most = 8 * device_sm_count();
   const unsigned blocks = (unsigned)(all < most ? all : most);
   // Counts of several blocks: up to eight are one cluster and sum them there, more
-  // add them to zeros that a launch of its own wrote (T = 64, E = 128: a call 10.2 us with
-  // two launches, 7.4 with one; replayed in a graph 4.4 and 4.6).
-  const bool clustered = load && blocks > 1 && blocks <= 8;
+  // add them to zeros that a launch of its own wrote; so do fewer in a graph, whose replay
+  // hides that launch and not the cluster's barriers.  With a cluster and with two
+  // launches, E = 128: a call 6.2 and 8.3 us at T = 9 to 64; replayed T = 9 4.4 and 4.3, T = 33 4.9
+  // and 4.3, T = 64 4.5 and 4.3; E = 256 in groups, replayed T = 33 6.5 and 6.0.
+  bool clustered = load && blocks > 1 && blocks <= 8;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (clustered && cudaStreamIsCapturing(stream, &capture) == cudaSuccess &&
+      capture == cudaStreamCaptureStatusActive)
+    clustered = false;
   if (load && blocks != 1 && !clustered &&
       launch_ex(zero_load_kernel, dim3(1), dim3(256), 0, stream, true, load, E) != cudaSuccess)
     return MOE_ERR_CUDA;

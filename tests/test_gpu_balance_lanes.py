@@ -44,3 +44,28 @@ def test_few_lanes_in_play(api, E, k, n_group, topk_group, T, scoring):
     assert np.array_equal(ids.cpu().numpy(), want_ids)
     assert np.array_equal(load.cpu().numpy(), want_load)
     assert (np.abs(w.cpu().numpy().astype(np.float64) - want) <= RTOL * want + ATOL).all()
+
+
+@pytest.mark.parametrize("T", [9, 33, 64])
+def test_the_load_of_few_blocks_called_and_replayed(api, T):
+    # called they are a cluster that sums the counts, in a graph they add to zeros
+    E, k = 128, 8
+    g = np.random.default_rng(T)
+    z = torch.zeros(T, E, device="cuda")
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    load = torch.full((E,), -5, dtype=torch.int32, device="cuda")
+    s = api.make_shape(T=T, H=8, E=E, k=k, I=8)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.moe_route_balanced(s, z, None, None, ids, w, load=load)
+    for _ in range(3):
+        new = g.standard_normal((T, E)).astype(np.float32)
+        want_ids, _, want_load = ref.route(new, k)
+        z.copy_(torch.from_numpy(new))
+        for go in (graph.replay, lambda: api.moe_route_balanced(s, z, None, None, ids, w, load=load)):
+            ids.fill_(-5)
+            load.fill_(-5)
+            go()
+            assert np.array_equal(ids.cpu().numpy(), want_ids)
+            assert np.array_equal(load.cpu().numpy(), want_load)
