@@ -74,21 +74,33 @@ LinPlan plan_linear(int64_t T, int NO, int K, bool gated, int sms, F at_once) {
   // eight while the blocks are few, or read weights in two places (gated).  In us with
   // sixteen, with eight and on the tcgen05 forms, T = 1: gated 2816 x 4224 4.1, 6.1, 6.1;
   // 4096 x 4096 5.8, 7.4, 6.9; 2048 x 8192 6.5, 5.6, 6.7; 3584 x 10000 12.4, 8.6, 10.1;
-  // 4096 x 14336 16.7, 15.2, 12.9; gated 4096 x 14336 15.4, 12.1, 13.6; gated 4096 x 28672
-  // 26.0, 20.2, 21.1; 8192 x 1024 7.2, 12.2, 5.9; gated 8192 x 28672 45.7, 41.4, 38.3.  A
-  // second tile of tokens pays for small weights alone, since every block reads all
+  // 4096 x 14336 16.7, 15.7, 13.7; gated 4096 x 14336 15.4, 12.1, 13.8; 8192 x 1024 7.2, 12.2,
+  // 5.9.  A second tile of tokens pays for small weights alone, since every block reads all
   // tokens (T = 16, sixteen and tcgen05: gated 2816 x 4224 5.8 and 6.1, 2112 x 2816 4.2
   // and 5.3, 4096 x 14336 20.1 and 12.9).
+  // Gated, the last round decides: eight blocks of eight warps are on an SM at once, and three
+  // tiles of the tcgen05 form.  With eight warps and on tcgen05, T = 1, gated 4096 x N:
+  // N = 18944 (a whole round of blocks) 14.8 and 17.1, 19456 18.5 and 16.1, 21504 19.1 and
+  // 17.7, 23040 19.6 and 19.6, 28672 21.5 and 22.8, 37888 (two rounds) 26.8 and 28.5, 40960
+  // 30.8 and 29.7, 45056 32.1 and 32.4, 57344 (a little over three rounds and one) 41.9 and
+  // 47.6; 2048 x 19456 10.6 and 9.8, x 28672 12.5 and 13.1; 1024 x 19456 6.8 and 6.8.  For longer
+  // K tcgen05, but for a short last round of its own: 5120 x 51200 43.8 and 43.9, x 65536 55.3
+  // and 60.7; 8192 x 28672 43.0 and 41.4, x 56832 76.3 and 72.7, x 57344 83.3 and 89.4, x 65536
+  // 86.0 and 92.1, x 75776 101 and 97.6; 16384 x 57344 157 and 171.
   const int blocks = ceil_div(NO, gated ? 8 : 16);
+  const int mt128 = ceil_div(NO, rows);
+  const int block_rest = blocks % (8 * sms), tile_rest = mt128 % (3 * sms);
+  const bool short_blocks = K >= 2048 && block_rest > 0 && 2 * block_rest <= 3 * sms;
+  const bool short_tiles = mt128 > 3 * sms && tile_rest > 0 && 2 * tile_rest <= sms;
   if (K <= 4096 && blocks <= 2 * sms && T <= 16)
     p.few = 16;
-  else if (K <= 4096 && (gated || blocks <= 5 * sms) && T <= 8)
+  else if (T <= 8 && (gated ? short_tiles || (K <= 4096 && !short_blocks)
+                            : K <= 4096 && blocks <= 5 * sms))
     p.few = 8;
   p.blocks = blocks;
   if (p.few) return p;
   p.cg = 1;
   p.KB = ceil_div(K, 128);
-  const int mt128 = ceil_div(NO, rows);
   // Tiles of 128 weight rows and up to 128 tokens, K split as far as the clusters all
   // run at once, a CTA to an SM (on B200 15 clusters of eight, 33 of four, 74 of two:
   // not all SMs are in full clusters).  K = 8192, T = 64, in us with 1, 2, 4 and 8 CTAs:
