@@ -26,6 +26,9 @@ CPU baseline and ``parity``: the layer outputs the oracle computed for the
 baseline's token sample set beside the GPU's (max |err| / RMS of the fp32
 and bf16 outputs), and the routing ids, gate weights and layout of the whole
 batch compared with the oracle's.  The headline carries the same ``parity``.
+The printed line holds each other workload's time, roofline fraction and parity verdict
+alone, so that it stays short enough for readers of the last few thousand characters of a
+log; ``--details FILE`` writes everything.
 ``--headline-only`` leaves the other workloads out; ``--fp8`` runs the
 headline with FP8 experts (``moe_forward_fp8``, prefill path).
 
@@ -86,10 +89,34 @@ def parse():
                     help="FP8 experts (e4m3 weights with per-row scales, moe_forward_fp8)")
     ap.add_argument("--headline-only", action="store_true",
                     help="skip the other workloads' lines (the configs key)")
+    ap.add_argument("--details", metavar="FILE",
+                    help="write the full records of all workloads as JSON")
     ap.add_argument("--router", action="store_true",
                     help="start from hidden states: the router (RMSNorm, scale, "
                          "GateLinear) computes the logits inside every step")
     return ap.parse_args()
+
+
+def line_of(result):
+    """The printed form of a result: floats to seven digits, the other workloads as
+    {"ms", "frac" (of the roofline), "parity"}, the parity record without the text of its
+    tolerance."""
+    def short(v):
+        if isinstance(v, float):
+            return float(f"{v:.7g}")
+        if isinstance(v, dict):
+            return {k: short(x) for k, x in v.items()}
+        return [short(x) for x in v] if isinstance(v, (list, tuple)) else v
+
+    line = short(result)
+    if line.get("parity"):
+        line["parity"].pop("tolerance", None)
+    if line.get("configs"):
+        line["configs"] = {
+            name: {"ms": float(f"{c['ms_per_step']:.4g}"),
+                   "frac": round(c["roofline"]["frac"], 3), "parity": c["parity"]["pass"]}
+            for name, c in line["configs"].items()}
+    return line
 
 
 def make_workload(args, device, seed):
@@ -992,7 +1019,10 @@ def run_ours(args):
                 for name in OTHER_CONFIGS}
             result["gpu_launches"] += sum(c["gpu_launches"]
                                           for c in result["configs"].values())
-        print(json.dumps(result), flush=True)
+        if args.details:
+            with open(args.details, "w") as f:
+                json.dump(result, f, indent=1)
+        print(json.dumps(line_of(result)), flush=True)
     if world > 1:
         dist.barrier()
         dist.destroy_process_group()
