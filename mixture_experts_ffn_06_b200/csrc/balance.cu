@@ -16,9 +16,10 @@
 // maximum over the LT heads, and a group of one lane has its two largest in
 // front.  Bound by the instructions per expert (score and sort) and their latencies,
 // then by the k rounds; the bytes (4 E + 8 k per token) would take a fifteenth of
-// the time.  B200, device time: T = 16384, E = 64, k = 6 10.3 us (484 GB/s; 5.7 million warp
-// instructions, issued in 54 % of the cycles); T = 4095, E = 256, k = 8 in 8 groups
-// 10.6 us; T = 64, E = 128 4.6 us; T = 1, E = 256 in groups 5.1 us.
+// the time.  B200, device time: T = 16384, E = 64, k = 6 11.2 us (446 GB/s; 5.7 million warp
+// instructions, issued in 53 % of the cycles); T = 4095, E = 256, k = 8 in 8 groups
+// 11.5 us (19 % of the issue slots: latency); T = 64, E = 128 4.6 us; T = 1, E = 256 in
+// groups 5.1 us.
 #include <cfloat>
 #include <cmath>
 

@@ -12,20 +12,19 @@
 //
 // Which form runs depends on what bounds it (linear_plan.cuh has the rules):
 //   few tokens, streaming w: small independent blocks with mma.sync
-//               (linear_i8_few_kernel; gated 4096 x 28672, T = 1: 20.2 us, 5.8 TB/s, 88 % of
+//               (linear_i8_few_kernel; gated 4096 x 28672, T = 1: 20.5 us, 5.7 TB/s, 87 % of
 //               the measured copy bandwidth);
 //   fewer tiles than SMs and K long enough: a tile per cluster of up to 8 CTAs that
 //               split K; each parks its partial sums in shared memory and adds
 //               up a slice of the columns over all CTAs' (integers: the order
-//               of the sum does not matter; gated 2816 x 4224, T = 64: 6.8 us, latency);
+//               of the sum does not matter; gated 2816 x 4224, T = 64: 7.3 us, latency);
 //   up to 128 tokens otherwise, streaming w: a CTA per tile, two or three to an SM
-//               (gated 4096 x 28672, T = 64: 21.5 us, 5.6 TB/s);
+//               (gated 4096 x 28672, T = 64: 21.9 us, 5.4 TB/s);
 //   more (bound by the tensor cores, under the power limit): persistent CTAs or
 //               CTA pairs (M = 256) walk the tiles, two accumulators in TMEM so
 //               that a tile's epilogue runs beside the next one's MMAs, or one of
 //               twice the columns, which reads each weight tile half as often (gated
-//               4096 x 28672, T = 4096: 284 to 305 us, 3.2 to 3.4 POPS; in a long run under the
-//               power limit 350 us, 2.75 POPS).
+//               4096 x 28672, T = 4096: 284 to 341 us, 2.8 to 3.4 POPS, by the power limit).
 // The tcgen05 forms have one TMA warp, one MMA warp and 4, 8 or 16 epilogue warps.
 // Every mbarrier wait is bounded (tc_ptx.cuh); after a timeout the block
 // records MOE_ERR_TIMEOUT, waits for its own copies and MMAs and frees TMEM.

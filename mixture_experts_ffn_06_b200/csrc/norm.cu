@@ -11,8 +11,8 @@
 // 16-byte vector, VPT vectors per thread) through its up to three reductions,
 // so every input byte is read once and every output byte written once.  B200:
 // T = 8192, H = 2816, both norms 35.3 us (5.2 TB/s, 80 % of the measured copy bandwidth);
-// T = 16383, H = 2048, with codes 61.5 us (4.9 TB/s; the instructions of the rounding to
-// codes come next, issued in 68 % of the cycles); T = 1 2.7 us.
+// T = 16383, H = 2048, with codes 58.6 us (5.1 TB/s; the instructions of the rounding to
+// codes come next, issued in 68 % of the cycles); T = 1 2.6 us.
 //
 // The means are taken in double (a square of a bf16 value is exact in fp32), and with IEEE
 // divisions and square roots the rows and their codes come out the same bits as the steps
